@@ -57,7 +57,9 @@ typedef enum {
     QK_ERR_NO_DEVICE = 4,         /* no CUDA device, or it is not sm_100       */
     QK_ERR_WORKSPACE = 5,         /* workspace too small or misaligned         */
     QK_ERR_CUDA = 6,              /* a CUDA runtime call or launch failed      */
-    QK_ERR_TIMEOUT = 7            /* a kernel wait gave up (device error word) */
+    QK_ERR_TIMEOUT = 7,           /* a kernel wait gave up (device error word) */
+    QK_ERR_INDEX = 8              /* a length, row bound or page id in device  */
+                                  /* memory is out of range (error word)       */
 } qk_status;
 
 /* Routes of the W4A8 product. */
@@ -407,6 +409,8 @@ qk_status qk_w4a8_linear_prepared(const uint16_t *x, int64_t M, int64_t K,
 /*
  * Synchronizes `stream`, then reads and clears this device's error word.
  * Returns QK_ERR_TIMEOUT if a kernel wait gave up since the last check,
+ * QK_ERR_INDEX if a kernel met a length, row bound or page id out of range
+ * (the 4-bit cache's calls; the first of the two that happened is kept),
  * QK_ERR_CUDA if the synchronization failed, else QK_OK.
  */
 qk_status qk_check_device_error(qk_stream_t stream);
@@ -445,6 +449,190 @@ qk_status qk_sage_attention(const uint16_t *q, const uint16_t *k, const uint16_t
                             int64_t B, int64_t H, int64_t L, int64_t D, float scale,
                             uint16_t *out, void *workspace, size_t ws_bytes,
                             qk_stream_t stream);
+
+/* ---------------------------------------------------- norm to int8 codes */
+
+/*
+ * RMS norm with the residual's addition, written as what the quantized
+ * products read (the layer in front of qk_w8a8_gemm and qk_w4a8_gemm; the
+ * pages' linears quantize a bf16 row of their own, "qlip-mlx" README,
+ * "w8a8_linear", and this keeps that row from being written).  Per row:
+ *   h    = bf16(x + residual)                (h = x without a residual)
+ *   u_k  = fl32(h_k weight_k)                (u = h without a weight)
+ *   U    = max_k |u_k|;  rstd = 1 / sqrt(sum_k h_k^2 / K + eps)
+ *   xq_k = round-half-even(fl32(u_k fl32(127 fl32(1 / U)))) clamped to [-127, 127]
+ *   sx   = fl32(fl32(U / 127) rstd);  an all-zero u gets sx = 1, codes 0
+ *   xsum[m, g] = sum of the codes of group g of 64, when xsum is not NULL
+ * so that xq sx is the norm h rstd weight in 8 bits.  The row's rstd cancels in
+ * the codes, which are exact: only sx depends on the fp32 sum of squares.
+ *   x        : bf16 bits [M, K]  (in)
+ *   residual : bf16 bits [M, K]  (in, nullable)
+ *   weight   : fp32 [K]          (in, nullable: ones)
+ *   eps      : finite, >= 0
+ *   h        : bf16 bits [M, K]  (out, with a residual only: the new residual
+ *              stream; NULL without).  h may be x or residual itself.
+ *   xq, sx   : int8 [M, K], fp32 [M]  (out)
+ *   xsum     : int32 [M, K/64]   (out, nullable; needs K % 64 == 0)
+ * Shape contract: 32 <= K <= 65536, K % 32 == 0, M >= 0.  Row sums of h^2 must
+ * stay within fp32, and |u| within the rows' range of the activation
+ * quantization.  All pointers 16-byte aligned.
+ */
+qk_status qk_rmsnorm_quantize(const uint16_t *x, const uint16_t *residual, int64_t M, int64_t K,
+                              const float *weight, float eps, uint16_t *h, int8_t *xq,
+                              float *sx, int32_t *xsum, qk_stream_t stream);
+
+/* ------------------------------------------------------ rotary positions */
+
+/* Which elements of a head form pair i (i < rot / 2). */
+typedef enum {
+    QK_ROPE_HALF = 0,       /* i and i + rot / 2 */
+    QK_ROPE_INTERLEAVED = 1 /* 2 i and 2 i + 1   */
+} qk_rope_layout;
+
+/* How the frequencies are stretched for contexts beyond the trained length. */
+typedef enum {
+    QK_ROPE_PLAIN = 0,   /* f_i = base^(-2 i / rot) / (2 pi)                        */
+    QK_ROPE_LINEAR = 1,  /* f_i / factor: positions interpolated                    */
+    QK_ROPE_NTK = 2,     /* base -> base factor^(rot / (rot - 2))  (rot > 2)        */
+    QK_ROPE_BY_PARTS = 3 /* kept where pair i turns >= fast times over the trained  */
+                         /* length, divided by factor where <= slow times, between  */
+                         /* them linear in the number of turns                      */
+} qk_rope_scaling;
+
+/*
+ * The frequencies of the rot / 2 pairs, in turns per position, fp64.
+ *   rot     : rotated dims, even, 2 .. 1024
+ *   base    : > 1; factor > 0 (read by every scaling but QK_ROPE_PLAIN);
+ *             trained > 0 and 0 <= slow < fast (read by QK_ROPE_BY_PARTS)
+ *   freq    : fp64 [rot / 2]  (out)
+ */
+qk_status qk_rope_frequencies(int64_t rot, double base, int scaling, double factor,
+                              double trained, double slow, double fast, double *freq,
+                              qk_stream_t stream);
+
+/*
+ * Rotary positions on T rows of H query heads and Hkv key heads of D dims (the
+ * views that a fused projection's output holds):
+ *   angle = 2 pi frac(positions[t] freq[i])   (product and fraction in fp64)
+ *   y_a = x_a c - x_b s,  y_b = x_b c + x_a s,  (c, s) = amplitude (cos, sin)
+ * for pair (a, b) of `layout` within the first rot dims of each head; the other
+ * dims are copied.  fp32, rounded once to bf16.
+ *   q        : bf16 bits, row t at q + t q_stride, its H heads contiguous (in)
+ *   q_out    : likewise with q_out_stride (out); may be q itself with the same
+ *              stride (in place), else it must not overlap q, k or k_out
+ *   k, k_out : the same for Hkv heads; NULL (both) for none
+ *   positions: int32 [T], any value  (in)
+ *   freq     : fp64 [rot / 2]        (in)
+ *   amplitude: finite (1, or the factor that a scaling asks for)
+ * Shape contract: T >= 0, H >= 1, 8 <= D <= 1024 with D % 8 == 0, 2 <= rot <= D
+ * even, strides >= heads D and multiples of 8, (H + Hkv) D < 2^26.  16-byte
+ * alignment.
+ */
+qk_status qk_rope(const uint16_t *q, int64_t q_stride, uint16_t *q_out, int64_t q_out_stride,
+                  int64_t H, const uint16_t *k, int64_t k_stride, uint16_t *k_out,
+                  int64_t k_out_stride, int64_t Hkv, int64_t T, int64_t D, int64_t rot,
+                  int layout, const int32_t *positions, const double *freq, float amplitude,
+                  qk_stream_t stream);
+
+/* --------------------------------------------- 4-bit key / value cache */
+
+/*
+ * A paged key / value cache in the affine group-64 format of the W4 weights
+ * ("qlip-mlx" README, "w4a8_linear"), one group = 64 dims of one token's K or V
+ * of one head: 9 D / 8 bytes per token and kv head for K and V together, where
+ * bf16 takes 4 D.  (The attention page among the sources, "MLX PR #3026",
+ * reads quantized K and V for decode.)
+ *
+ * The cache is [num_pages, Hkv, page, D + D/8] bytes, page a multiple of 16:
+ * per page and kv head one record of 18 D bytes for every 16 tokens, NG = D/64:
+ *   K codes  [row 16][t 4][group NG][j 2] 4-byte words, nibble i of a word =
+ *            dim 64 group + 16 t + 8 j + i of token `row`
+ *   V codes  [pair 8][g 8][group NG][h 2] 4-byte words, low half = token 2 pair,
+ *            high half = token 2 pair + 1, nibble i of a half = dim
+ *            64 group + 8 g + 4 h + i
+ *   K scales [token 16][group NG] fp16 (scale, offset); V scales likewise
+ * (the order in which the attention's tensor-core operands take them).  It needs
+ * no initial value: only tokens that were appended are read.
+ *
+ * Common arguments, all int32 in device memory:
+ *   page_table : [B, max_pages], page of token p of request b at
+ *                [b, p / page]; entries that no token needs may hold anything.
+ *   kv_lens    : [B], tokens of each request, the call's rows included.
+ *   cu_rows    : [B + 1], the call's rows of request b are cu_rows[b] ..
+ *                cu_rows[b + 1] - 1 (non-decreasing, within [0, T]): the LAST
+ *                tokens of the request, row r of n at position kv_len - n + r.
+ *                NULL: T / B rows each (T % B == 0).  Rows in front of cu_rows[0]
+ *                or from cu_rows[B] on belong to nobody and are left alone.
+ * The host cannot see these.  A kernel that meets one out of range (a kv_len
+ * below 0 or above max_pages page, a row bound outside [0, T] or falling, a
+ * page id outside [0, num_pages) under a token that is needed, an appended row at
+ * a negative position) records QK_ERR_INDEX for qk_check_device_error and skips
+ * that token: nothing outside the buffers is read or written.
+ * Shape contract: D = 64 or 128; page % 16 == 0, 16 <= page <= 1024;
+ * Hkv >= 1; 1 <= num_pages, max_pages; max_pages page <= 2^30; T <= 2^30; B >= 1
+ * (T = 0 is a no-op).  16-byte alignment; row strides (in elements) >= heads D
+ * and multiples of 8.
+ */
+
+/* Bytes of a cache, or 0 outside the contract. */
+size_t qk_kv4_cache_size(int64_t num_pages, int64_t Hkv, int64_t page, int64_t D);
+
+/*
+ * Writes T rows of keys and values (Hkv heads each, bf16 bits, row t at
+ * k + t k_stride) as the tokens that cu_rows and kv_lens give them.  Per group:
+ * the rule of qk_quantize_weights_int4 on the bf16 values (|w| < 65504).  Two
+ * rows that land on one token leave one of the two there, whole or mixed.
+ */
+qk_status qk_kv4_append(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                        int64_t T, int64_t Hkv, int64_t D, const int32_t *page_table, int64_t B,
+                        int64_t max_pages, const int32_t *kv_lens, const int32_t *cu_rows,
+                        void *cache, int64_t num_pages, int64_t page, qk_stream_t stream);
+
+/*
+ * Reads tokens back: the value code scale + offset (fp32, rounded once to bf16)
+ * of the tokens that cu_rows and kv_lens name (all of a request where its rows
+ * number kv_len), into rows of Hkv heads.  A row whose token is out of range
+ * comes back as zeros.
+ */
+qk_status qk_kv4_gather(const void *cache, int64_t num_pages, int64_t page, int64_t Hkv, int64_t D,
+                        const int32_t *page_table, int64_t B, int64_t max_pages,
+                        const int32_t *kv_lens, const int32_t *cu_rows, int64_t T, uint16_t *k,
+                        int64_t k_stride, uint16_t *v, int64_t v_stride, qk_stream_t stream);
+
+/* Bytes of workspace qk_kv4_attention needs (the same for every batch), or 0
+ * for a head dim outside the contract. */
+size_t qk_kv4_attention_workspace_size(int64_t D);
+
+/*
+ * Causal attention of each request's rows over its tokens in the cache.  The
+ * row at position p sees the keys j <= p; with window > 0 only those with
+ * j > p - window or j < sinks.
+ *   out_i = sum_j softmax_j(scale q_i . k_j) v_j,  k, v = code scale + offset
+ * Query head h reads kv head h / (H / Hkv).  q . code is exact products summed in
+ * fp32, the softmax and its sums are fp32, the weights enter the second product
+ * with 16 bits of significand, and out is rounded once to bf16: the error is
+ * that rounding plus at most about 2^-15 of the values' range (and the scores'
+ * fp32 sums).  Deterministic; a request's result does not depend on the rest
+ * of the batch beyond the order in which its parts are joined.
+ *   q         : bf16 bits, row t at q + t q_stride, H heads of D (in)
+ *   scale     : finite, >= 0;  window, sinks: >= 0 (window = 0: all keys),
+ *               at most 2^30
+ *   out       : bf16 bits [T, H, D], contiguous (out; must not overlap q).
+ *               Rows that see no key are 0.
+ *   workspace : >= qk_kv4_attention_workspace_size(D) bytes, 256-byte aligned,
+ *               or NULL (allocated stream-ordered).  Calls that may overlap need
+ *               workspaces of their own.  Nothing in it is kept.
+ * Pages in front of every row's window (and behind the sinks) are not read and
+ * may be freed.  (H / Hkv) T < 2^31.
+ * Kernels: the attention (one block per SM, equal spans of the cache) and the
+ * join of what was cut between blocks.
+ */
+qk_status qk_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t T, int64_t H, int64_t Hkv,
+                           int64_t D, const void *cache, int64_t num_pages, int64_t page,
+                           const int32_t *page_table, int64_t B, int64_t max_pages,
+                           const int32_t *kv_lens, const int32_t *cu_rows, float scale,
+                           int64_t window, int64_t sinks, uint16_t *out, void *workspace,
+                           size_t ws_bytes, qk_stream_t stream);
 
 /* ------------------------------------------------------------ test hooks */
 

@@ -23,6 +23,7 @@ if not os.path.exists(_LIB_PATH):
 lib = ctypes.CDLL(_LIB_PATH)
 
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_F, _D = ctypes.c_float, ctypes.c_double
 _SIGS = {
     "qk_status_string": (ctypes.c_char_p, [_I]),
     "qk_version": (_I, []),
@@ -53,6 +54,18 @@ _SIGS = {
     "qk_debug_w4a8_plane_count": (_I, [_P, _P, _I64, _I64, _P, _P, _P]),
     "qk_sage_attention_workspace_size": (_SZ, [_I64, _I64, _I64]),
     "qk_sage_attention": (_I, [_P, _P, _P, _I64, _I64, _I64, _I64, ctypes.c_float, _P, _P, _SZ, _P]),
+    "qk_rmsnorm_quantize": (_I, [_P, _P, _I64, _I64, _P, _F, _P, _P, _P, _P, _P]),
+    "qk_rope_frequencies": (_I, [_I64, _D, _I, _D, _D, _D, _D, _P, _P]),
+    "qk_rope": (_I, [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I, _P,
+                     _P, _F, _P]),
+    "qk_kv4_cache_size": (_SZ, [_I64, _I64, _I64, _I64]),
+    "qk_kv4_append": (_I, [_P, _I64, _P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64,
+                           _I64, _P]),
+    "qk_kv4_gather": (_I, [_P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _I64, _P,
+                           _I64, _P]),
+    "qk_kv4_attention_workspace_size": (_SZ, [_I64]),
+    "qk_kv4_attention": (_I, [_P, _I64, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P,
+                              _P, _F, _I64, _I64, _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -61,6 +74,8 @@ for _name, (_res, _args) in _SIGS.items():
 
 QK_OK = 0
 QK_ROUTE_AUTO, QK_ROUTE_GEMM, QK_ROUTE_GEMV, QK_ROUTE_GEMM_FOLD = 0, 1, 2, 3
+QK_ROPE_HALF, QK_ROPE_INTERLEAVED = 0, 1
+QK_ROPE_PLAIN, QK_ROPE_LINEAR, QK_ROPE_NTK, QK_ROPE_BY_PARTS = 0, 1, 2, 3
 QK_PLAN_NONE, QK_PLAN_GEMV_QUANT, QK_PLAN_QUANT_GEMV, QK_PLAN_QUANT_GEMM = 0, 1, 2, 3
 
 
@@ -427,4 +442,205 @@ def qk_sage_attention(q, k, v, scale=None, out=None, workspace=None, stream=None
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.qk_sage_attention(_ptr(q), _ptr(k), _ptr(v), B, H, L, D, float(scale), _ptr(out),
                                  _ptr(workspace), ws_bytes, _stream(stream)), "qk_sage_attention")
+    return out
+
+
+# ---------------------------------------- norm, rotary positions, 4-bit cache
+
+def _same_device(**tensors) -> None:
+    """Every tensor on the current CUDA device, where the kernels launch."""
+    here = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != here:
+            raise ValueError(f"{name} is on {t.device}, and the current device is cuda:{here}")
+
+
+def _rows(t, heads, D, name):
+    """A bf16 [T, heads, D] view whose heads lie next to each other (rows of a
+    larger projection may lie further apart); returns its row stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, D):
+        raise ValueError(f"{name} must have shape [T, {heads}, {D}], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.shape[0] == 0:
+        return heads * D
+    if (D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(heads * D, t.stride(0))
+
+
+def qk_rmsnorm_quantize(x, weight=None, residual=None, eps=1e-6, h=None, xq=None, sx=None,
+                        xsum=None, with_xsum=False, stream=None):
+    """x bf16 [M, K] (+ residual) -> (h, xq int8 [M, K], sx fp32 [M], xsum int32 [M, K/64] or
+    None): the RMS norm of h = x + residual times weight (fp32 [K]) as codes and scales, for
+    qk_w8a8_gemm and qk_w4a8_gemm.  h (bf16) is the new residual stream, None without a residual;
+    h may be x or residual itself."""
+    _need(x, torch.bfloat16, 2, "x")
+    M, K = x.shape
+    if weight is not None:
+        _need(weight, torch.float32, 1, "weight")
+        if weight.shape[0] != K:
+            raise ValueError(f"weight must have shape [{K}]")
+    if residual is not None:
+        _need(residual, torch.bfloat16, 2, "residual")
+        if residual.shape != x.shape:
+            raise ValueError("residual must have x's shape")
+        h = _out(h, (M, K), torch.bfloat16, x.device, "h")
+    elif h is not None:
+        raise ValueError("h is written with a residual only")
+    xq = _out(xq, (M, K), torch.int8, x.device, "xq")
+    sx = _out(sx, (M,), torch.float32, x.device, "sx")
+    if with_xsum or xsum is not None:
+        xsum = _out(xsum, (M, K // 64), torch.int32, x.device, "xsum")
+    _same_device(x=x, weight=weight, residual=residual, h=h, xq=xq, sx=sx, xsum=xsum)
+    _check(lib.qk_rmsnorm_quantize(_ptr(x), _ptr(residual), M, K, _ptr(weight), float(eps), _ptr(h),
+                                   _ptr(xq), _ptr(sx), _ptr(xsum), _stream(stream)),
+           "qk_rmsnorm_quantize")
+    return h, xq, sx, xsum
+
+
+def qk_rope_frequencies(rot, base=10000.0, scaling=QK_ROPE_PLAIN, factor=1.0, trained=0.0, slow=1.0,
+                        fast=32.0, freq=None, stream=None):
+    """fp64 [rot / 2]: turns per position of each pair (see include/qk.h for the scalings)."""
+    if freq is None:
+        freq = torch.empty(rot // 2, dtype=torch.float64, device="cuda")
+    else:
+        _need(freq, torch.float64, 1, "freq")
+        if freq.shape[0] != rot // 2:
+            raise ValueError(f"freq must have shape [{rot // 2}]")
+    _same_device(freq=freq)
+    _check(lib.qk_rope_frequencies(int(rot), float(base), int(scaling), float(factor),
+                                   float(trained), float(slow), float(fast), _ptr(freq),
+                                   _stream(stream)), "qk_rope_frequencies")
+    return freq
+
+
+def qk_rope(q, k, positions, freq, layout=QK_ROPE_HALF, amplitude=1.0, q_out=None, k_out=None,
+            stream=None):
+    """Rotary positions on q bf16 [T, H, D] and k bf16 [T, Hkv, D] (or None), positions int32 [T],
+    the first 2 len(freq) dims of each head; returns (q_out, k_out).  Rows may be strided; q_out=q
+    (k_out=k) turns them in place."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [T, H, D] tensor")
+    T, H, D = q.shape
+    qs = _rows(q, H, D, "q")
+    _need(positions, torch.int32, 1, "positions")
+    _need(freq, torch.float64, 1, "freq")
+    if positions.shape[0] != T:
+        raise ValueError(f"positions must have shape [{T}]")
+    if q_out is None:
+        q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+    qos = _rows(q_out, H, D, "q_out")
+    Hkv = ks = kos = 0
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise ValueError("k must be a [T, Hkv, D] tensor")
+        Hkv = k.shape[1]
+        ks = _rows(k, Hkv, D, "k")
+        if k_out is None:
+            k_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=k.device)
+        kos = _rows(k_out, Hkv, D, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if any(t is not None and t.shape[0] != T for t in (k, q_out, k_out)):
+        raise ValueError("q, k and the outputs must have the same number of rows")
+    _same_device(q=q, k=k, positions=positions, freq=freq, q_out=q_out, k_out=k_out)
+    _check(lib.qk_rope(_ptr(q), qs, _ptr(q_out), qos, H, _ptr(k), ks, _ptr(k_out), kos, Hkv, T, D,
+                       2 * freq.shape[0], int(layout), _ptr(positions), _ptr(freq),
+                       float(amplitude), _stream(stream)), "qk_rope")
+    return q_out, k_out
+
+
+def qk_kv4_cache_size(num_pages: int, Hkv: int, page: int, D: int) -> int:
+    return int(lib.qk_kv4_cache_size(int(num_pages), int(Hkv), int(page), int(D)))
+
+
+def qk_kv4_attention_workspace_size(D: int) -> int:
+    return int(lib.qk_kv4_attention_workspace_size(int(D)))
+
+
+def _kv4(cache, page_table, kv_lens, cu_rows, T):
+    """(Hkv, D, B, max_pages, num_pages, page) of a cache uint8 [num_pages, Hkv, page, D + D/8]
+    and its requests."""
+    _need(cache, torch.uint8, 4, "cache")
+    _need(page_table, torch.int32, 2, "page_table")
+    _need(kv_lens, torch.int32, 1, "kv_lens")
+    num_pages, Hkv, page, width = cache.shape
+    if width % 9 != 0:
+        raise ValueError("cache must have shape [num_pages, Hkv, page, D + D / 8]")
+    B, max_pages = page_table.shape
+    if kv_lens.shape[0] != B:
+        raise ValueError(f"kv_lens must have shape [{B}]")
+    if cu_rows is not None:
+        _need(cu_rows, torch.int32, 1, "cu_rows")
+        if cu_rows.shape[0] != B + 1:
+            raise ValueError(f"cu_rows must have shape [{B + 1}]")
+    elif B == 0 or T % B != 0:
+        raise ValueError("without cu_rows every request has the same number of rows")
+    _same_device(cache=cache, page_table=page_table, kv_lens=kv_lens, cu_rows=cu_rows)
+    return Hkv, width // 9 * 8, B, max_pages, num_pages, page
+
+
+def qk_kv4_append(k, v, cache, page_table, kv_lens, cu_rows=None, stream=None):
+    """Writes k, v bf16 [T, Hkv, D] into the 4-bit cache uint8 [num_pages, Hkv, page, D + D/8] as
+    the last tokens of their requests: page_table int32 [B, max_pages], kv_lens int32 [B] (new
+    tokens included), cu_rows int32 [B + 1] (rows of each request; None: T / B each)."""
+    T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
+    Hkv, D, B, max_pages, num_pages, page = _kv4(cache, page_table, kv_lens, cu_rows, T)
+    ks, vs = _rows(k, Hkv, D, "k"), _rows(v, Hkv, D, "v")
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same number of rows")
+    _same_device(k=k, v=v)
+    _check(lib.qk_kv4_append(_ptr(k), ks, _ptr(v), vs, T, Hkv, D, _ptr(page_table), B, max_pages,
+                             _ptr(kv_lens), _ptr(cu_rows), _ptr(cache), num_pages, page,
+                             _stream(stream)), "qk_kv4_append")
+
+
+def qk_kv4_gather(cache, page_table, kv_lens, cu_rows, T, k=None, v=None, stream=None):
+    """(k, v) bf16 [T, Hkv, D]: the values of the last tokens of each request (cu_rows as in
+    qk_kv4_append; all of them where a request's rows number its length)."""
+    T = int(T)
+    Hkv, D, B, max_pages, num_pages, page = _kv4(cache, page_table, kv_lens, cu_rows, T)
+    if k is None:
+        k = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=cache.device)
+    if v is None:
+        v = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=cache.device)
+    ks, vs = _rows(k, Hkv, D, "k"), _rows(v, Hkv, D, "v")
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError(f"k and v must have {T} rows")
+    _same_device(k=k, v=v)
+    _check(lib.qk_kv4_gather(_ptr(cache), num_pages, page, Hkv, D, _ptr(page_table), B, max_pages,
+                             _ptr(kv_lens), _ptr(cu_rows), T, _ptr(k), ks, _ptr(v), vs,
+                             _stream(stream)), "qk_kv4_gather")
+    return k, v
+
+
+def qk_kv4_attention(q, cache, page_table, kv_lens, cu_rows=None, scale=None, window=0, sinks=0,
+                     out=None, workspace=None, stream=None):
+    """Causal attention of q bf16 [T, H, D] (the last tokens of each request, already appended)
+    over the 4-bit cache; returns bf16 [T, H, D].  window > 0: only the last `window` keys and the
+    first `sinks` ones.  Without a workspace, one is taken from torch's allocator (on the current
+    stream) or, for another stream, allocated in its order."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [T, H, D] tensor")
+    T, H = q.shape[0], q.shape[1]
+    Hkv, D, B, max_pages, num_pages, page = _kv4(cache, page_table, kv_lens, cu_rows, T)
+    qs = _rows(q, H, D, "q")
+    out = _out(out, (T, H, D), torch.bfloat16, q.device, "out")
+    s = _stream(stream)
+    if workspace is None and s == torch.cuda.current_stream().cuda_stream:
+        workspace = torch.empty(max(1, lib.qk_kv4_attention_workspace_size(D)), dtype=torch.uint8,
+                                device=q.device)
+    if scale is None:
+        scale = D ** -0.5
+    _same_device(q=q, out=out, workspace=workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.qk_kv4_attention(_ptr(q), qs, T, H, Hkv, D, _ptr(cache), num_pages, page,
+                                _ptr(page_table), B, max_pages, _ptr(kv_lens), _ptr(cu_rows),
+                                float(scale), int(window), int(sinks), _ptr(out), _ptr(workspace),
+                                ws_bytes, s), "qk_kv4_attention")
     return out

@@ -207,6 +207,7 @@ const char* qk_status_string(int status) {
     case QK_ERR_WORKSPACE: return "QK_ERR_WORKSPACE: workspace too small or not 256-byte aligned";
     case QK_ERR_CUDA: return "QK_ERR_CUDA: a CUDA call or kernel launch failed";
     case QK_ERR_TIMEOUT: return "QK_ERR_TIMEOUT: a kernel wait gave up";
+    case QK_ERR_INDEX: return "QK_ERR_INDEX: a length, row bound or page id is out of range";
     default: return "unknown qk_status";
   }
 }
@@ -574,7 +575,7 @@ qk_status qk_check_device_error(qk_stream_t stream) {
     if ((st = from_cuda(cudaMemcpy(word, &zero, sizeof zero, cudaMemcpyHostToDevice),
                         "clear error word")) != QK_OK)
       return st;
-    return h == QK_ERR_TIMEOUT ? QK_ERR_TIMEOUT : QK_ERR_CUDA;
+    return h == QK_ERR_TIMEOUT || h == QK_ERR_INDEX ? (qk_status)h : QK_ERR_CUDA;
   }
   return QK_OK;
 }
@@ -637,6 +638,214 @@ qk_status qk_sage_attention(const uint16_t* q, const uint16_t* k, const uint16_t
       (st = from_cuda(launch_transpose_v(v, BH, L, vt, stream), "transpose_v")) == QK_OK)
     st = from_cuda(launch_sage_attention(qc, sq, kc, sk, vt, BH, L, scale, out, stream),
                    "sage_attention");
+  if (owned != nullptr) cudaFreeAsync(owned, stream);
+  return st;
+}
+
+// ---- norm, rotary positions, 4-bit cache
+
+qk_status qk_rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, int64_t M, int64_t K,
+                              const float* weight, float eps, uint16_t* h, int8_t* xq, float* sx,
+                              int32_t* xsum, qk_stream_t stream) {
+  if (M < 0 || K < 0 || !(eps >= 0.0f) || !(eps < INFINITY)) return QK_ERR_INVALID_ARG;
+  if (K < 32 || K > 65536 || K % 32 != 0 || M > INT32_MAX) return QK_ERR_UNSUPPORTED_SHAPE;
+  if (xsum != nullptr && K % 64 != 0) return QK_ERR_UNSUPPORTED_SHAPE;
+  if ((residual == nullptr) != (h == nullptr) && M > 0) return QK_ERR_INVALID_ARG;
+  if (M == 0) return QK_OK;
+  if (!x || !xq || !sx) return QK_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(h) ||
+      !aligned16(xq) || !aligned16(sx) || !aligned16(xsum))
+    return QK_ERR_MISALIGNED;
+  qk_status st = check_device();
+  if (st != QK_OK) return st;
+  if (log_enabled())
+    std::fprintf(stderr, "[qk] rmsnorm_quantize M=%lld K=%lld\n", (long long)M, (long long)K);
+  return from_cuda(launch_norm_quant(x, residual, M, K, weight, eps, h, xq, sx, xsum, stream),
+                   "norm_quant");
+}
+
+qk_status qk_rope_frequencies(int64_t rot, double base, int scaling, double factor, double trained,
+                              double slow, double fast, double* freq, qk_stream_t stream) {
+  if (scaling < QK_ROPE_PLAIN || scaling > QK_ROPE_BY_PARTS) return QK_ERR_INVALID_ARG;
+  if (!(base > 1.0) || !(base < INFINITY)) return QK_ERR_INVALID_ARG;
+  if (scaling != QK_ROPE_PLAIN && (!(factor > 0.0) || !(factor < INFINITY)))
+    return QK_ERR_INVALID_ARG;
+  if (scaling == QK_ROPE_BY_PARTS &&
+      (!(trained > 0.0) || !(trained < INFINITY) || !(slow >= 0.0) || !(fast > slow) ||
+       !(fast < INFINITY)))
+    return QK_ERR_INVALID_ARG;
+  if (rot < 2 || rot > 1024 || rot % 2 != 0) return QK_ERR_UNSUPPORTED_SHAPE;
+  if (!freq) return QK_ERR_INVALID_ARG;
+  if (!aligned16(freq)) return QK_ERR_MISALIGNED;
+  qk_status st = check_device();
+  if (st != QK_OK) return st;
+  return from_cuda(launch_rope_frequencies(rot, base, scaling, factor, trained, slow, fast, freq,
+                                           stream),
+                   "rope_frequencies");
+}
+
+qk_status qk_rope(const uint16_t* q, int64_t q_stride, uint16_t* q_out, int64_t q_out_stride,
+                  int64_t H, const uint16_t* k, int64_t k_stride, uint16_t* k_out,
+                  int64_t k_out_stride, int64_t Hkv, int64_t T, int64_t D, int64_t rot, int layout,
+                  const int32_t* positions, const double* freq, float amplitude,
+                  qk_stream_t stream) {
+  if (T < 0 || H < 1 || (layout != QK_ROPE_HALF && layout != QK_ROPE_INTERLEAVED) ||
+      !(amplitude > -INFINITY) || !(amplitude < INFINITY))
+    return QK_ERR_INVALID_ARG;
+  if ((k == nullptr) != (k_out == nullptr) || (k != nullptr && Hkv < 1)) return QK_ERR_INVALID_ARG;
+  const int64_t hk = k != nullptr ? Hkv : 0;
+  if (T > INT32_MAX || D < 8 || D > 1024 || D % 8 != 0 || rot < 2 || rot > D || rot % 2 != 0 ||
+      H > (int64_t(1) << 26) || hk > (int64_t(1) << 26) || (H + hk) * D >= (int64_t(1) << 26))
+    return QK_ERR_UNSUPPORTED_SHAPE;
+  if (q_stride < H * D || q_out_stride < H * D || q_stride % 8 != 0 || q_out_stride % 8 != 0)
+    return QK_ERR_UNSUPPORTED_SHAPE;
+  if (hk > 0 && (k_stride < hk * D || k_out_stride < hk * D || k_stride % 8 != 0 ||
+                 k_out_stride % 8 != 0))
+    return QK_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return QK_OK;
+  if (!q || !q_out || !positions || !freq) return QK_ERR_INVALID_ARG;
+  if ((q == q_out && q_stride != q_out_stride) || (hk > 0 && k == k_out && k_stride != k_out_stride))
+    return QK_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out) ||
+      !aligned16(positions) || !aligned16(freq))
+    return QK_ERR_MISALIGNED;
+  qk_status st = check_device();
+  if (st != QK_OK) return st;
+  if (log_enabled())
+    std::fprintf(stderr, "[qk] rope T=%lld H=%lld+%lld D=%lld rot=%lld\n", (long long)T,
+                 (long long)H, (long long)hk, (long long)D, (long long)rot);
+  return from_cuda(launch_rope(q, q_stride, q_out, q_out_stride, H, k, k_stride, k_out,
+                               k_out_stride, hk, T, D, rot, layout == QK_ROPE_HALF, positions, freq,
+                               amplitude, stream),
+                   "rope");
+}
+
+// The cache's shape contract.
+static bool kv4_shape_ok(int64_t num_pages, int64_t Hkv, int64_t page, int64_t D) {
+  return (D == 64 || D == 128) && page >= 16 && page <= 1024 && page % 16 == 0 && Hkv >= 1 &&
+         Hkv <= 65536 && num_pages >= 1 && num_pages <= INT32_MAX;
+}
+
+// The arguments that the cache's three calls share.
+static qk_status kv4_check(int64_t T, int64_t Hkv, int64_t D, const int32_t* page_table, int64_t B,
+                           int64_t max_pages, const int32_t* kv_lens, const int32_t* cu_rows,
+                           const void* cache, int64_t num_pages, int64_t page) {
+  if (T < 0 || B < 0 || max_pages < 0 || num_pages < 0) return QK_ERR_INVALID_ARG;
+  if (!kv4_shape_ok(num_pages, Hkv, page, D) || T > (int64_t(1) << 30) || B > (int64_t(1) << 30) ||
+      max_pages < 1 || max_pages > (int64_t(1) << 30) / page)
+    return QK_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return QK_OK;
+  if (B < 1 || !page_table || !kv_lens || !cache) return QK_ERR_INVALID_ARG;
+  if (cu_rows == nullptr && T % B != 0) return QK_ERR_INVALID_ARG;
+  if (!aligned16(page_table) || !aligned16(kv_lens) || !aligned16(cu_rows) || !aligned16(cache))
+    return QK_ERR_MISALIGNED;
+  return QK_OK;
+}
+
+static Kv4Req kv4_req(int64_t T, const int32_t* page_table, int64_t B, int64_t max_pages,
+                      const int32_t* kv_lens, const int32_t* cu_rows, int64_t page) {
+  return Kv4Req{page_table, kv_lens, cu_rows, (int)B, (int)T, (int)max_pages,
+                (int)(max_pages * page)};
+}
+
+size_t qk_kv4_cache_size(int64_t num_pages, int64_t Hkv, int64_t page, int64_t D) {
+  if (!kv4_shape_ok(num_pages, Hkv, page, D)) return 0;
+  return (size_t)num_pages * (size_t)Hkv * (size_t)page * (size_t)(D + D / 8);
+}
+
+qk_status qk_kv4_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                        int64_t T, int64_t Hkv, int64_t D, const int32_t* page_table, int64_t B,
+                        int64_t max_pages, const int32_t* kv_lens, const int32_t* cu_rows,
+                        void* cache, int64_t num_pages, int64_t page, qk_stream_t stream) {
+  qk_status st =
+      kv4_check(T, Hkv, D, page_table, B, max_pages, kv_lens, cu_rows, cache, num_pages, page);
+  if (st != QK_OK) return st;
+  if (k_stride < Hkv * D || v_stride < Hkv * D || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return QK_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return QK_OK;
+  if (!k || !v) return QK_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v)) return QK_ERR_MISALIGNED;
+  if ((st = check_device()) != QK_OK) return st;
+  int* err = device_error_word();
+  if (err == nullptr) return QK_ERR_CUDA;
+  if (log_enabled())
+    std::fprintf(stderr, "[qk] kv4_append T=%lld B=%lld Hkv=%lld D=%lld\n", (long long)T,
+                 (long long)B, (long long)Hkv, (long long)D);
+  return from_cuda(
+      launch_kv4_append(k, k_stride, v, v_stride,
+                        kv4_req(T, page_table, B, max_pages, kv_lens, cu_rows, page),
+                        Kv4Cache{static_cast<uint8_t*>(cache), (int)num_pages, (int)Hkv, (int)D,
+                                 (int)page},
+                        err, stream),
+      "kv4_append");
+}
+
+qk_status qk_kv4_gather(const void* cache, int64_t num_pages, int64_t page, int64_t Hkv, int64_t D,
+                        const int32_t* page_table, int64_t B, int64_t max_pages,
+                        const int32_t* kv_lens, const int32_t* cu_rows, int64_t T, uint16_t* k,
+                        int64_t k_stride, uint16_t* v, int64_t v_stride, qk_stream_t stream) {
+  qk_status st =
+      kv4_check(T, Hkv, D, page_table, B, max_pages, kv_lens, cu_rows, cache, num_pages, page);
+  if (st != QK_OK) return st;
+  if (k_stride < Hkv * D || v_stride < Hkv * D || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return QK_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return QK_OK;
+  if (!k || !v) return QK_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v)) return QK_ERR_MISALIGNED;
+  if ((st = check_device()) != QK_OK) return st;
+  int* err = device_error_word();
+  if (err == nullptr) return QK_ERR_CUDA;
+  uint8_t* base = const_cast<uint8_t*>(static_cast<const uint8_t*>(cache));  // only read
+  return from_cuda(
+      launch_kv4_gather(kv4_req(T, page_table, B, max_pages, kv_lens, cu_rows, page),
+                        Kv4Cache{base, (int)num_pages, (int)Hkv, (int)D, (int)page}, k, k_stride, v,
+                        v_stride, err, stream),
+      "kv4_gather");
+}
+
+size_t qk_kv4_attention_workspace_size(int64_t D) {
+  return D == 64 || D == 128 ? round256(kv4_attention_workspace(D)) : 0;
+}
+
+qk_status qk_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t H, int64_t Hkv,
+                           int64_t D, const void* cache, int64_t num_pages, int64_t page,
+                           const int32_t* page_table, int64_t B, int64_t max_pages,
+                           const int32_t* kv_lens, const int32_t* cu_rows, float scale,
+                           int64_t window, int64_t sinks, uint16_t* out, void* workspace,
+                           size_t ws_bytes, qk_stream_t stream) {
+  if (!(scale >= 0.0f) || !(scale < INFINITY) || window < 0 || sinks < 0) return QK_ERR_INVALID_ARG;
+  qk_status st =
+      kv4_check(T, Hkv, D, page_table, B, max_pages, kv_lens, cu_rows, cache, num_pages, page);
+  if (st != QK_OK) return st;
+  if (H < 1 || H > INT32_MAX || H % Hkv != 0 || H / Hkv * T > INT32_MAX ||
+      window > (int64_t(1) << 30) || sinks > (int64_t(1) << 30) || q_stride < H * D ||
+      q_stride % 8 != 0)
+    return QK_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return QK_OK;
+  if (!q || !out) return QK_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return QK_ERR_MISALIGNED;
+  const size_t need = qk_kv4_attention_workspace_size(D);
+  if (workspace != nullptr && (ws_bytes < need || !aligned256(workspace))) return QK_ERR_WORKSPACE;
+  if ((st = check_device()) != QK_OK) return st;
+  int* err = device_error_word();
+  if (err == nullptr) return QK_ERR_CUDA;
+  void* owned = nullptr;
+  if (workspace == nullptr) {
+    if ((st = from_cuda(cudaMallocAsync(&owned, need, stream), "cudaMallocAsync(workspace)")) !=
+        QK_OK)
+      return st;
+    workspace = owned;
+  }
+  if (log_enabled())
+    std::fprintf(stderr, "[qk] kv4_attention T=%lld B=%lld H=%lld/%lld D=%lld\n", (long long)T,
+                 (long long)B, (long long)H, (long long)Hkv, (long long)D);
+  uint8_t* base = const_cast<uint8_t*>(static_cast<const uint8_t*>(cache));  // only read
+  st = from_cuda(
+      launch_kv4_attention(q, q_stride, H,
+                           kv4_req(T, page_table, B, max_pages, kv_lens, cu_rows, page),
+                           Kv4Cache{base, (int)num_pages, (int)Hkv, (int)D, (int)page}, scale,
+                           window, sinks, out, workspace, err, stream),
+      "kv4_attention");
   if (owned != nullptr) cudaFreeAsync(owned, stream);
   return st;
 }

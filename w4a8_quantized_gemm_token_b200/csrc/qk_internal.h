@@ -63,6 +63,48 @@ cudaError_t launch_sage_attention(const int8_t* qc, const float* sq, const int8_
 cudaError_t launch_transpose_v(const uint16_t* v, int64_t BH, int64_t L, uint16_t* vt,
                                cudaStream_t s);
 
+// RMS norm with the residual's addition and int8 codes (norm_quant.cu); residual
+// (with h), weight and xsum may be null.
+cudaError_t launch_norm_quant(const uint16_t* x, const uint16_t* residual, int64_t M, int64_t K,
+                              const float* weight, float eps, uint16_t* h, int8_t* xq, float* sx,
+                              int32_t* xsum, cudaStream_t s);
+
+// Rotary positions (rope.cu); k may be null.  Strides in elements between tokens.
+cudaError_t launch_rope(const uint16_t* q, int64_t q_stride, uint16_t* q_out, int64_t q_out_stride,
+                        int64_t H, const uint16_t* k, int64_t k_stride, uint16_t* k_out,
+                        int64_t k_out_stride, int64_t Hkv, int64_t T, int64_t D, int64_t rot,
+                        bool half, const int32_t* positions, const double* freq, float amplitude,
+                        cudaStream_t s);
+cudaError_t launch_rope_frequencies(int64_t rot, double base, int scaling, double factor,
+                                    double trained, double slow, double fast, double* freq,
+                                    cudaStream_t s);
+
+// The requests of a 4-bit cache call: T rows, request b's being [cu[b], cu[b + 1])
+// (T / B each without cu), the last ones of its kv_lens[b] tokens.
+struct Kv4Req {
+  const int32_t* page_table;  // [B, max_pages]
+  const int32_t* kv_lens;     // [B]
+  const int32_t* cu;          // [B + 1] or null
+  int B, T, max_pages;
+  int max_len;                // max_pages * page
+};
+// The cache (layout in kv4.cuh).
+struct Kv4Cache {
+  uint8_t* base;
+  int num_pages, Hkv, D, page;
+};
+
+cudaError_t launch_kv4_append(const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                              int64_t v_stride, const Kv4Req& req, const Kv4Cache& cache, int* err,
+                              cudaStream_t s);
+cudaError_t launch_kv4_gather(const Kv4Req& req, const Kv4Cache& cache, uint16_t* k,
+                              int64_t k_stride, uint16_t* v, int64_t v_stride, int* err,
+                              cudaStream_t s);
+size_t kv4_attention_workspace(int64_t D);
+cudaError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t H, const Kv4Req& req,
+                                 const Kv4Cache& cache, float scale, int64_t window, int64_t sinks,
+                                 uint16_t* out, void* workspace, int* err, cudaStream_t s);
+
 // Test hook: one kernel whose two waits can never complete, each bounded by
 // `limit_cycles`; both record QK_ERR_TIMEOUT (debug_wait.cu).
 cudaError_t launch_wait_timeout_probe(long long limit_cycles, cudaStream_t s);
