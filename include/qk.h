@@ -609,10 +609,10 @@ size_t qk_kv4_attention_workspace_size(int64_t D);
  * j > p - window or j < sinks.
  *   out_i = sum_j softmax_j(scale q_i . k_j) v_j,  k, v = code scale + offset
  * Query head h reads kv head h / (H / Hkv).  q . code is exact products summed in
- * fp32, the softmax and its sums are fp32, the weights enter the second product
- * with 16 bits of significand, and out is rounded once to bf16: the error is
- * that rounding plus at most about 2^-15 of the values' range (and the scores'
- * fp32 sums).  Deterministic; a request's result does not depend on the rest
+ * fp32, the softmax and its sums are fp32, a weight times its value's scale enters
+ * the second product as fp16 (11 bits), and out is rounded once to bf16: the
+ * error is that rounding plus at most about 2^-11 sum_j P_j 15 scale_j (and the
+ * scores' fp32 sums).  Deterministic; a request's result does not depend on the rest
  * of the batch beyond the order in which its parts are joined.
  *   q         : bf16 bits, row t at q + t q_stride, H heads of D (in)
  *   scale     : finite, >= 0;  window, sinks: >= 0 (window = 0: all keys),
@@ -623,7 +623,7 @@ size_t qk_kv4_attention_workspace_size(int64_t D);
  *               or NULL (allocated stream-ordered).  Calls that may overlap need
  *               workspaces of their own.  Nothing in it is kept.
  * Pages in front of every row's window (and behind the sinks) are not read and
- * may be freed.  (H / Hkv) T < 2^31.
+ * may be freed.  (H / Hkv) T <= 2^30.
  * Kernels: the attention (one block per SM, equal spans of the cache) and the
  * join of what was cut between blocks.
  */

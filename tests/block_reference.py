@@ -102,7 +102,7 @@ def request_kv(cache, table_row, length, D):
 
 def attention(q, k, v, scale, window, sinks):
     """q [n, H, D], k, v fp64 [L, Hkv, D] (the rows are the last n tokens) -> (out fp64, how far a
-    result computed with fp32 scores, fp32 sums and weights of 15 bits may be from it)."""
+    result computed with fp32 scores and sums, and weight x scale rounded to fp16, may be from it)."""
     n, H, D = q.shape
     L, Hkv = k.shape[:2]
     G = H // Hkv
@@ -126,7 +126,8 @@ def attention(q, k, v, scale, window, sinks):
     a = scale * torch.einsum("ihd,jhd->hij", q.to(F64).abs(), kk.abs()).masked_fill(~see, 0).amax(-1)
     a = 3 * a.T[..., None]  # bounds scale sum |q| (|code scale| + |offset|): 3 |k| as for the values
     # scores: 64 products and 4 group terms per sum, then one product: 2^-17 a; the weights move by
-    # twice that, plus 2^-15 (two bf16 halves), 2^-21 (2^x, the sum of the weights);
-    # fp32 sums of P V: two roundings per 16 keys and the join's
-    move = 2 * a * 2.0 ** -17 + 2.0 ** -14 + (2 * (L / 16) + 400) * 2.0 ** -23
+    # twice that and by 2^-20 (2^x, the sum of the weights).  weight x scale is rounded to fp16, half
+    # a step 2^-11 of it: sum P scale code 2^-11 <= 2^-11 spread.  fp32 sums of P V: two roundings per
+    # 16 keys and the join's
+    move = 2 * a * 2.0 ** -17 + 2.0 ** -20 + 2.0 ** -11 + (2 * (L / 16) + 400) * 2.0 ** -23
     return out, 2.0 ** -8 * out.abs() + spread * move

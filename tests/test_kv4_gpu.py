@@ -266,6 +266,80 @@ def test_closed_forms(qk):  # noqa: F811
     assert ((out[0, 0].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * part).all()
 
 
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 3), (128, 12)])
+def test_value_scales_far_apart(qk, D, G):  # noqa: F811
+    """Value scales over fp16's range (as far as the offsets are finite), in every order of size and score, heads of one key
+    among them: every output within the rounding of its own sum P scale code."""
+    g = torch.Generator(device="cuda").manual_seed(D + G)
+    lens = [700, 90, 333]
+    n = sum(lens)
+    for trend in (-1, 0, 1, 2):
+        c = Batch(qk, lens, [1, 2, 1], 2, D, 16, seed=trend + 5, fill=False)
+        at = torch.cat([torch.linspace(0, 1, m, device="cuda") for m in lens])
+        if trend == 0:
+            at = torch.rand(n, generator=g, device="cuda")
+        if trend == 2:  # a first token of huge values, then tiny ones
+            at = torch.where(at == 0, 1.0, 0.3)
+        size = torch.exp2(-20 + 33 * (at if trend >= 0 else 1 - at))[:, None, None]
+        v = (torch.randn(n, 2, D, generator=g, device="cuda") * size).bfloat16()
+        v[5::7] = 0.0
+        k = torch.randn(n, 2, D, generator=g, device="cuda").bfloat16()
+        qk.qk_kv4_append(k, v, c.cache, c.table, c.lens, i32([0, 700, 790, 1123]))
+        for strength in (0.0, 1.0, 8.0):
+            q = (c.randn(c.T, 2 * G, D) * strength).bfloat16()
+            out = qk.qk_kv4_attention(q, c.cache, c.table, c.lens, c.cu)
+            first = 0
+            for b, m in enumerate(lens):
+                kk, vv = ref.request_kv(c.cache, c.table[b], m, D)
+                _, _, s, o = ref.quantize4(v[first:first + m])
+                first += m
+                reach = (15 * s + o.abs()).repeat_interleave(64, -1)  # of a key's codes and offset
+                rows = q[c.first[b]:c.first[b + 1]]
+                want, _ = ref.attention(rows, kk, vv, D ** -0.5, 0, 0)
+                part, _ = ref.attention(rows, kk, reach, D ** -0.5, 0, 0)  # sum P (15 scale + |offset|)
+                a = 3 * D ** -0.5 * rows.double().abs().sum(-1).amax() * kk.abs().amax()
+                # P scale as fp16: 2^-11 of itself, or 2^-25 where the row's largest is at least 2^9: m
+                # times 2^-34 of the largest; scores (2^-17 a each way), 2^x, fp32 sums as in ref.attention
+                move = 2.0 ** -11 + m * 2.0 ** -34 + 2 * a * 2.0 ** -17 + 2.0 ** -20 + (m / 8 + 400) * 2.0 ** -23
+                got = out[c.first[b]:c.first[b + 1]].double()
+                assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + part * move).all(), (trend, strength, b)
+    qk.qk_check_device_error()
+
+
+def test_infinite_values_stay_in_their_group(qk):  # noqa: F811
+    """A visible token whose value group holds infinities makes that group NaN, and nothing else."""
+    c = Batch(qk, [300, 40], [1, 1], 1, 128, 16, seed=3)
+    q = c.q(4)
+    clean = qk.qk_kv4_attention(q, c.cache, c.table, c.lens, c.cu)
+    x = c.randn(1, 1, 128).bfloat16()
+    k, v = ref.request_kv(c.cache, c.table[0], 300, 128)
+    place = c.table[0, 2:3, None].clone()  # token 37 of request 0, by a table of its own page
+    kk = k[37:38].bfloat16()
+    vv = v[37:38].bfloat16()
+    vv[0, 0, 3] = float("inf")
+    vv[0, 0, 64:] = x[0, 0, 64:]
+    qk.qk_kv4_append(kk, vv, c.cache, place, i32([6]))
+    out = qk.qk_kv4_attention(q, c.cache, c.table, c.lens, c.cu)
+    assert torch.equal(bits(out[1]), bits(clean[1]))
+    assert torch.isnan(out[0, :, :64]).all()
+    k, v = ref.request_kv(c.cache, c.table[0], 300, 128)
+    want, tol = ref.attention(q[:1], k, v.nan_to_num(0, 0, 0), 128 ** -0.5, 0, 0)
+    assert ((out[0, :, 64:].double() - want[0, :, 64:]).abs() <= tol[0, :, 64:]).all()
+    qk.qk_check_device_error()
+
+
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 4)])
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -30, 1.0, 2.0 ** 30, 2.0 ** 100])
+def test_query_sizes(qk, D, G, size):  # noqa: F811
+    """Rows of any magnitude, with the scale that brings the scores back."""
+    c = Batch(qk, [100, 17], [3, 1], 2, D, 16, seed=G)
+    q = (c.randn(c.T, 2 * G, D) * size).bfloat16()
+    scale = min(D ** -0.5 / size, 2.0 ** 98)
+    out = qk.qk_kv4_attention(q, c.cache, c.table, c.lens, c.cu, scale=scale)
+    c.check(q, out, scale=scale)
+    qk.qk_check_device_error()
+
+
 def test_strided_queries(qk):  # noqa: F811
     c = Batch(qk, [100, 37], [2, 3], 2, 64, 16)
     rows = c.randn(c.T, 6 * 64 + 40).bfloat16()
@@ -331,7 +405,8 @@ def test_bad_pages_and_lengths(qk):  # noqa: F811
         out = qk.qk_kv4_attention(q, c.cache, c.table, i32(lens), c.cu)
         with pytest.raises(qk.QKError):
             qk.qk_check_device_error()
-        assert torch.equal(bits(out[1]), bits(good[1]))
+        # (the others' lengths move where request 1 is cut, and with it the order of its sums)
+        c.check(q, out, requests=[1])
     # row bounds that fall, or leave the rows
     for cu in ([0, 1, 0, 2], [0, 1, 2, 99], [-3, 1, 2, 4]):
         qk.qk_kv4_attention(q, c.cache, c.table, c.lens, i32(cu))

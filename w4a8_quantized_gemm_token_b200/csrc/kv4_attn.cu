@@ -6,20 +6,28 @@
 // over the visible keys j <= p with j > p - window or j < sinks:
 //     x_j = scale sum_groups [ sK_jg (q_g . cK_jg) + oK_jg sum(q_g) ]
 //     P_j = 2^((x_j - max) log2 e),   l = sum_j P_j
-//     out = 1/l sum_j P_j (sV_jg cV_j + oV_jg)
-// The codes (0..15) are exact in bf16, so the tensor cores take them as they are:
-// q . c is exact products summed in fp32, and no dequantized K or V exists
-// anywhere.  P_j sV_jg is split into two bf16 (16 bits of significand) and both
-// halves are multiplied; rounding it once to bf16 would cost more than the
-// output's own rounding, since P sV c and P oV nearly cancel.
+//     out = 1/l sum_j [ (P_j sV_jg) cV_j + P_j oV_jg ]
+// No dequantized K or V exists anywhere.  A code 0..15 in bits 0-3 of an fp16 word
+// of exponent 0 is the subnormal c 2^-24, in bits 4-7 it is 16 c 2^-24: one
+// and-mask turns two nibbles of a word into an operand pair, and five instructions
+// (a shift by 8 and four masks) a word of 8 codes into four.  The 16 goes into q
+// (K) or into the end of the sums (V).  The other operands are fp16 too:
+//  * q, times a power of two per row that puts its largest element into
+//    [2^13, 2^14): exact, but for elements 2^-23 below the largest;
+//  * P sV: a row's reference is its maximum less what puts the largest P sV of the
+//    record where it was set into [2^9, 2^10); a product of 2^15 or more lowers it in
+//    the same way.  So P sV has 11 bits of significand down to 2^-23 of one that the
+//    row has met, and an error of 2^-34 of that one below.  P oV and l stay in fp32.
+// Sums are fp32 throughout.
 //
-// Bound: HBM (9 D / 8 bytes per visible token and kv head).  What has to keep up
-// with it is the integer and fp32 work per code: 11 instructions unpack a word of
-// 8 codes into the four bf16 pairs of a fragment (three shifts, four and-or with
-// the exponent of 128, four subtractions of 128).  mma.sync is used rather than
-// tcgen05 because its operands are registers: a tcgen05 tile of 128 would have to
-// write the unpacked codes to shared memory (4 bytes per code written and read,
-// against half a byte loaded) to multiply them with the 1 to 16 rows there are.
+// Bound: HBM (9 D / 8 bytes per visible token and kv head); what has to keep up
+// with it is the issue of instructions, about 220 per record of 16 tokens and warp.
+// mma.sync is used rather than tcgen05 because its operands are registers: a
+// tcgen05 tile of 128 would have to write the unpacked codes to shared memory (2
+// bytes per code written and read, against half a byte loaded) to multiply them
+// with the 1 to 16 rows there are.  The codes are the operand of 16 rows (keys for
+// the scores, dims for the output) and the queries the one of 8 columns, so that
+// eight rows of queries waste nothing.
 //
 // Layout of the work: an item is (request, row tile, kv head), its units are the
 // 16-token records it sees.  All units of all items are laid end to end and cut
@@ -31,10 +39,8 @@
 // of the units: no atomics, the same bits on every run.
 //
 // One producer warp per block runs every consumer's ring of bulk copies (lane c
-// for consumer c): it walks the items, looks the pages up and keeps each ring full.
-//
-// A row tile is 16 rows (kWide) or 8: with 8 the tile's upper half of the
-// 16-row fragments holds the low halves of P sV, so that both halves cost one mma.
+// for consumer c): it walks the items, looks the pages up and keeps each ring
+// full.  The first copies of a span are issued by its consumer, a lane each.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -49,13 +55,14 @@ namespace {
 
 constexpr int kMaxBlocks = 160;  // a block per SM; the workspace holds this many
 
-template <int D, bool kWide>
+// NT tiles of 8 query rows per item.
+template <int D, int NT>
 struct Cfg {
-  static constexpr int ROWS = kWide ? 16 : 8;
-  // 11 consumers and the producer: three warps to a quarter of the SM, 168
-  // registers a thread (a thirteenth warp would leave 128)
-  static constexpr int NW = 11;
-  static constexpr int STAGES = kWide ? 5 : 6;         // records in a consumer's ring
+  static constexpr int ROWS = 8 * NT;
+  // NT = 1: 15 consumers and the producer, four warps to a quarter of the SM (128
+  // registers a thread); NT = 2: 11 and the producer, three warps (168 registers)
+  static constexpr int NW = NT == 1 ? 15 : 11;
+  static constexpr int STAGES = 4;                     // records in a consumer's ring
   static constexpr int THREADS = 32 * (NW + 1);
   static constexpr int LD = D + 4;                     // floats per row of a piece in shared memory
   static constexpr int PIECE = (ROWS * LD + 2 * ROWS) * 4;  // O rows, then m, l
@@ -68,13 +75,30 @@ struct Cfg {
   static constexpr int SMEM = SM_SPAN + NW * 32 + 128;
   static_assert(PIECE <= RING, "a span's last piece is kept in its ring");
   static_assert(SM_HEAD % 16 == 0 && SM_BAR % 16 == 0 && SM_SPAN % 16 == 0, "alignment");
-  static_assert(SMEM + 8 * (THREADS + 64) <= 232448, "with the static shared memory");
+  static_assert(SMEM + 24 * (THREADS + 64) <= 232448, "with the static shared memory");
 };
+
+// n / d for n < 2^31 by a multiplication: 2^p / d rounded up, p = 31 + ceil(log2 d), is
+// off by less than 2^(p - 31) / n in the quotient.
+struct FastDiv {
+  uint32_t m, p;
+  int d;
+};
+FastDiv fast_div(int d) {
+  uint32_t l = 0;
+  while ((1ull << l) < (uint64_t)d) ++l;
+  const uint64_t two_p = 1ull << (31 + l);
+  return FastDiv{(uint32_t)((two_p + (uint64_t)d - 1) / (uint64_t)d), 31 + l, d};
+}
+__device__ __forceinline__ int quot(int n, const FastDiv& f) {
+  return (int)(((uint64_t)(uint32_t)n * f.m) >> f.p);
+}
 
 struct Args {
   const uint16_t* q;
   long long q_stride;
   int H, G;
+  FastDiv by_g, by_page;  // rows per token; records per page
   Kv4Req req;
   Kv4Cache cache;
   float sc;  // scale log2 e
@@ -105,32 +129,43 @@ struct Item {
   int row0, n, len, nrt;
   int cnt, ns, first;  // units, how many of them are sinks' records, first record behind those
   int p0, p1;          // positions of the tile's first and last row
+  int whole0, whole1;  // every row sees all 16 keys of units [whole0, whole1)
 };
 
 template <int ROWS>
-__device__ __forceinline__ void load_request(const Args& a, Item& it) {
-  const Kv4Seq s = kv4_seq(a.req, it.b, a.err);
+__device__ __forceinline__ void set_request(const Args& a, Item& it, const Kv4Seq& s) {
   it.row0 = s.row0;
   it.n = s.n;
   it.len = s.len;
-  it.nrt = (int)(((long long)s.n * a.G + ROWS - 1) / ROWS);
+  it.nrt = (s.n * a.G + ROWS - 1) / ROWS;
 }
 
-// The records that row tile rt of the loaded request sees; one empty unit where it sees none.
+template <int ROWS>
+__device__ __forceinline__ void load_request(const Args& a, Item& it) {
+  set_request<ROWS>(a, it, kv4_seq(a.req, it.b, a.err));
+}
+
+// The records that row tile rt of the request sees; one empty unit where it sees none.
 template <int ROWS>
 __device__ __forceinline__ void load_tile(const Args& a, Item& it) {
   const int last = it.n * a.G - 1;
-  it.p0 = it.len - it.n + it.rt * ROWS / a.G;
-  it.p1 = it.len - it.n + min(it.rt * ROWS + ROWS - 1, last) / a.G;
-  it.ns = it.first = 0;
+  it.p0 = it.len - it.n + quot(it.rt * ROWS, a.by_g);
+  it.p1 = it.len - it.n + quot(min(it.rt * ROWS + ROWS - 1, last), a.by_g);
+  it.ns = it.first = it.whole0 = it.whole1 = 0;
   it.cnt = 1;
   if (it.p1 < 0) return;
   const int end = (it.p1 >> 4) + 1;
   if (a.window > 0) {
     it.first = max(it.p0 - a.window + 1, 0) >> 4;
     it.ns = min((a.sinks + 15) >> 4, it.first);
+    it.whole0 = it.ns + ((max(it.p1 - a.window + 1, 0) + 15) >> 4) - it.first;
   }
   it.cnt = it.ns + end - it.first;
+  it.whole1 = max(it.ns + ((max(it.p0, -1) + 1) >> 4) - it.first, it.whole0);
+}
+
+__device__ __forceinline__ int record_of(const Item& it, int k) {
+  return k < it.ns ? k : it.first + k - it.ns;
 }
 
 // Steps to the next item (kv heads innermost, then row tiles, then requests).
@@ -154,7 +189,7 @@ __device__ __forceinline__ int warp_sum(int v) {
   return v;
 }
 
-// Units of all row tiles of the loaded request, for one kv head, by the whole warp.
+// Units of all row tiles of the request, for one kv head, by the whole warp.
 template <int ROWS>
 __device__ __forceinline__ long long request_units(const Args& a, const Item& base) {
   long long sum = 0;
@@ -173,9 +208,10 @@ __device__ __forceinline__ long long request_units(const Args& a, const Item& ba
 
 // What a consumer warp starts from, in shared memory for its producer lane.
 struct Span {
-  int b, rt, kvh, k;
   long long units;
-  int pad[2];
+  int b, rt, kvh, k;
+  int filled;  // units whose copies the consumer has issued
+  int pad;
 };
 static_assert(sizeof(Span) == 32, "span size");
 
@@ -197,64 +233,103 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// D += A B^T, 16 x 8 x 16, bf16 operands, fp32 sums.
+// D += A B, 16 x 8 x 16, fp16 operands, fp32 sums.
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Nibbles i and i + 4 of w as a pair of bf16: 0x4300 | c is 128 + c, less 128.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
-  uint32_t r = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-  const uint32_t base = 0x43004300u;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&r),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&base));
-  return *reinterpret_cast<const uint32_t*>(&d);
+// The transpose of an 8 x 8 matrix of 16-bit elements, two per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-
-// a, b as hi + lo, each a pair of bf16: hi truncates, lo rounds what is left.
-__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo) {
-  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-  *hi = __byte_perm(ua, ub, 0x7632);
-  *lo = pack16(a - __uint_as_float(ua & 0xFFFF0000u), b - __uint_as_float(ub & 0xFFFF0000u));
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 r = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ int exponent(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
 
 template <int N>
 __device__ __forceinline__ void lds(uint32_t (&r)[N], const uint8_t* p) {
-  static_assert(N == 2 || N == 4, "8 or 16 bytes");
+  static_assert(N == 1 || N == 2 || N == 4, "4, 8 or 16 bytes");
   if constexpr (N == 4) {
     const uint4 v = *reinterpret_cast<const uint4*>(p);
     r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
-  } else {
+  } else if constexpr (N == 2) {
     const uint2 v = *reinterpret_cast<const uint2*>(p);
     r[0] = v.x; r[1] = v.y;
+  } else {
+    r[0] = *reinterpret_cast<const uint32_t*>(p);
   }
 }
 
-constexpr float kNone = -1.0e30f;  // the reference maximum of a row that has seen nothing
+// The largest finite scale of a key's groups.
+template <int N>
+__device__ __forceinline__ float largest_scale(const uint32_t (&t)[N]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float s = unpack_f16(t[i]).x;
+    m = s < INFINITY ? fmaxf(m, s) : m;
+  }
+  return m;
+}
 
-template <int D, bool kWide>
-__global__ void __launch_bounds__(Cfg<D, kWide>::THREADS, 1) kv4_attn_kernel(const Args a, int min_units) {
-  using C = Cfg<D, kWide>;
+// Over the lanes of equal lane % 4: over the keys, for a query row's column.
+__device__ __forceinline__ float column_max(float v) {
+#pragma unroll
+  for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+  return v;
+}
+
+constexpr float kNone = -1.0e30f;   // the reference maximum of a row that has seen nothing
+constexpr float kLeast = -3.0e38f;  // the least one that is kept
+
+// Rows of P sV of 16 keys as fp16 (b0, b1 of the second product, one group).  With
+// masks, a key that a row does not see has weight 0 whatever its record holds.
+template <bool kMask>
+__device__ __forceinline__ void weigh(const float (&p)[4], float s0, float s1, uint32_t (&w)[2]) {
+  float v[4] = {p[0] * s0, p[1] * s0, p[2] * s1, p[3] * s1};
+  if (kMask) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = p[i] == 0.0f ? 0.0f : v[i];
+  }
+  w[0] = pack_f16(v[0], v[1]);
+  w[1] = pack_f16(v[2], v[3]);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const Args a, int min_units) {
+  using C = Cfg<D, NT>;
   using L = Kv4<D>;
   constexpr int NG = L::NG, ROWS = C::ROWS, NW = C::NW, STAGES = C::STAGES;
-  constexpr int RT = kWide ? 2 : 1;  // fragment row halves that hold rows of their own
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem<128>(smem_raw);
   __shared__ long long pre[C::THREADS + 1];
-  __shared__ int seg_flags[NW];
-  __shared__ int seg_item[NW][6];  // first piece's b, rt, kvh; last piece's
+  __shared__ Kv4Seq seqs[C::THREADS];
+  __shared__ long long tot[NW + 1];
+  __shared__ int seg_flags[32];
+  __shared__ int seg_item[NW][5];  // last piece's b, rt, kvh, row0, n
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int blk = blockIdx.x;
-  auto full = [&](int w, int s) { return smem_u32(smem + C::SM_BAR) + (uint32_t)(w * STAGES + s) * 16u; };
+  const uint32_t bars = smem_u32(smem + C::SM_BAR);
+  auto full = [&](int w, int s) { return bars + (uint32_t)(w * STAGES + s) * 16u; };
   auto empty = [&](int w, int s) { return full(w, s) + 8u; };
   int* bad = reinterpret_cast<int*>(smem + C::SM_BAD);
   Span* spans = reinterpret_cast<Span*>(smem + C::SM_SPAN);
@@ -262,8 +337,8 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::THREADS, 1) kv4_attn_kernel(con
   if (threadIdx.x < NW * STAGES) {
     mbar_init(full(0, threadIdx.x), 1);
     mbar_init(empty(0, threadIdx.x), 1);
+    fence_mbar_init();
   }
-  fence_mbar_init();
   pdl_launch_dependents();
   pdl_wait();
 
@@ -277,7 +352,9 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::THREADS, 1) kv4_attn_kernel(con
       it.nrt = 0;
       int one = 0;
       if (it.b < a.req.B) {
-        load_request<ROWS>(a, it);
+        const Kv4Seq sq = kv4_seq(a.req, it.b, a.err);
+        if (i == 0) seqs[threadIdx.x] = sq;  // the stretch's first request
+        set_request<ROWS>(a, it, sq);
         if (it.nrt == 1) {
           it.rt = 0;
           load_tile<ROWS>(a, it);
@@ -305,48 +382,59 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::THREADS, 1) kv4_attn_kernel(con
       const long long v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
       if (lane >= o) sum += v;
     }
-    __shared__ long long tot[NW + 1];
     if (lane == 31) tot[warp] = sum;
     __syncthreads();
     long long before = 0;
-    for (int w = 0; w < warp; ++w) before += tot[w];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) before += w < warp ? tot[w] : 0;
     pre[threadIdx.x + 1] = before + sum;
     if (threadIdx.x == 0) pre[0] = 0;
     __syncthreads();
   }
   const long long W = pre[C::THREADS];
-  const long long want = (W + (long long)NW * min_units - 1) / ((long long)NW * min_units);
-  const int blocks = (int)min((long long)gridDim.x, want);
+  // a block for every NW min_units units (a small count needs no 64-bit division)
+  const int blocks = W >= (long long)gridDim.x * NW * min_units
+                         ? (int)gridDim.x
+                         : ((int)W + NW * min_units - 1) / (NW * min_units);
   if (blk == 0 && threadIdx.x == 0) *reinterpret_cast<int*>(a.ws) = blocks;
   if (blk >= blocks) return;  // the whole block
 
+  Item it = {};
+  Span sp = {};
   if (warp < NW) {
-    // ---- this warp's span [u0, u1) and the item it starts in
-    const long long slot = (long long)blk * NW + warp, slots = (long long)blocks * NW;
-    const long long u0 = W * slot / slots, u1 = W * (slot + 1) / slots;
-    Span sp = {};
-    sp.units = u1 - u0;
+    // ---- this warp's span of W / slots units (one more for the first W % slots), and
+    // the item it starts in
+    const int slot = blk * NW + warp, slots = blocks * NW;
+    const long long each = W >> 31 ? W / slots : (long long)((uint32_t)W / (uint32_t)slots);
+    const int more = (int)(W - each * slots);
+    const long long u0 = each * slot + min(slot, more);
+    sp.units = each + (slot < more ? 1 : 0);
     if (sp.units > 0) {
-      int lo = 0, hi = C::THREADS - 1;  // the last t with pre[t] <= u0 and units behind it
+      int lo = 0, hi = C::THREADS - 1;  // the last t with pre[t] <= u0: it has units
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (pre[mid] <= u0) lo = mid; else hi = mid - 1;
       }
       long long rest = u0 - pre[lo];
-      Item it;
       it.b = lo * per;
-      for (;; ++it.b) {
-        load_request<ROWS>(a, it);
-        const long long u = request_units<ROWS>(a, it) * a.cache.Hkv;
-        if (rest < u || it.b + 1 >= a.req.B) break;
-        rest -= u;
+      set_request<ROWS>(a, it, seqs[lo]);
+      if (per > 1) {
+        for (;;) {
+          const long long u = request_units<ROWS>(a, it) * a.cache.Hkv;
+          if (rest < u || it.b + 1 >= a.req.B) break;
+          rest -= u;
+          ++it.b;
+          load_request<ROWS>(a, it);
+        }
       }
-      for (int rt0 = 0;; rt0 += 32) {
-        it.rt = rt0 + lane;
+      int at = 0;  // the row tile
+      for (int rt0 = 0; it.nrt > 1; rt0 += 32) {
+        Item one = it;
+        one.rt = rt0 + lane;
         long long c = 0;
-        if (it.rt < it.nrt) {
-          load_tile<ROWS>(a, it);
-          c = (long long)it.cnt * a.cache.Hkv;
+        if (one.rt < one.nrt) {
+          load_tile<ROWS>(a, one);
+          c = (long long)one.cnt * a.cache.Hkv;
         }
         long long sum = c;
 #pragma unroll
@@ -358,11 +446,7 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::THREADS, 1) kv4_attn_kernel(con
         if (over != 0) {
           const int src = __ffs(over) - 1;
           rest -= __shfl_sync(0xFFFFFFFFu, sum - c, src);
-          const int cnt = __shfl_sync(0xFFFFFFFFu, it.cnt, src);
-          sp.b = it.b;
-          sp.rt = rt0 + src;
-          sp.kvh = (int)(rest / cnt);
-          sp.k = (int)(rest - (long long)sp.kvh * cnt);
+          at = rt0 + src;
           break;
         }
         rest -= __shfl_sync(0xFFFFFFFFu, sum, 31);
@@ -371,73 +455,115 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::THREADS, 1) kv4_attn_kernel(con
           break;
         }
       }
+      it.rt = at;
+      load_tile<ROWS>(a, it);
+      it.kvh = rest >> 31 ? (int)(rest / it.cnt) : (int)((uint32_t)rest / (uint32_t)it.cnt);
+      sp.k = (int)(rest - (long long)it.kvh * it.cnt);
+      sp.b = it.b;
+      sp.rt = it.rt;
+      sp.kvh = it.kvh;
+      if (it.p1 >= 0) sp.filled = (int)min((long long)min(STAGES, it.cnt - sp.k), sp.units);
+    }
+    // the first copies, a lane each
+    if (lane < sp.filled) {
+      const int rec_no = record_of(it, sp.k + lane), pg = quot(rec_no, a.by_page);
+      const int id = __ldg(a.req.page_table + (long long)it.b * a.req.max_pages + pg);
+      const bool fits = id >= 0 && id < a.cache.num_pages;
+      bad[warp * STAGES + lane] = fits ? 0 : 1;
+      if (fits) {
+        const long long rec = ((long long)id * a.cache.Hkv + it.kvh) * a.by_page.d + rec_no - pg * a.by_page.d;
+        mbar_arrive_expect_tx(full(warp, lane), L::REC);
+        bulk_load(smem_u32(smem + C::SM_RING + warp * C::RING + lane * L::REC),
+                  a.cache.base + rec * L::REC, L::REC, full(warp, lane));
+      } else {
+        record_index(a.err);
+        mbar_arrive(full(warp, lane));
+      }
     }
     if (lane == 0) {
       spans[warp] = sp;
       seg_flags[warp] = 0;
     }
+  } else if (lane >= NW) {
+    seg_flags[lane] = 0;
   }
   __syncthreads();
 
-  const int tiles_per_page = a.cache.page >> 4;
   if (warp == NW) {
     // ------------------------------------------------------------- producer
     long long left = 0, issued = 0;
-    Item it = {};
-    int k = 0;
+    int k = 0, s = 0;
+    uint32_t ph = 1;
     if (lane < NW) {
-      const Span sp = spans[lane];
-      left = sp.units;
+      const Span mine = spans[lane];
+      left = mine.units - mine.filled;
+      issued = mine.filled;
+      if (mine.filled == STAGES) {
+        ph = 0;
+      } else {
+        s = mine.filled;
+      }
       if (left > 0) {
-        it.b = sp.b;
-        it.rt = sp.rt;
-        it.kvh = sp.kvh;
-        k = sp.k;
-        load_request<ROWS>(a, it);
+        it.b = mine.b;
+        it.rt = mine.rt;
+        it.kvh = mine.kvh;
+        k = mine.k + mine.filled;
+        if (per == 1)
+          set_request<ROWS>(a, it, seqs[it.b]);
+        else
+          load_request<ROWS>(a, it);
         load_tile<ROWS>(a, it);
+        if (k == it.cnt) {
+          k = 0;
+          next_item<ROWS>(a, it);
+        }
       }
     }
-    auto lookup = [&]() -> int {  // the next unit's page
+    int rec_no = 0, pg = 0;
+    auto lookup = [&]() -> int {  // the next unit's record and page
       if (left == 0 || it.p1 < 0) return -1;
-      const int tile = k < it.ns ? k : it.first + k - it.ns;
-      return __ldg(a.req.page_table + (long long)it.b * a.req.max_pages + tile / tiles_per_page);
+      rec_no = record_of(it, k);
+      pg = quot(rec_no, a.by_page);
+      return __ldg(a.req.page_table + (long long)it.b * a.req.max_pages + pg);
     };
     int id = lookup();
     long long t0 = clock64();
     while (__any_sync(0xFFFFFFFFu, left > 0)) {
       bool moved = false;
-      if (left > 0) {
-        const int s = (int)(issued % STAGES);
-        const uint32_t ph = (uint32_t)((issued / STAGES) & 1) ^ 1u;
-        if (mbar_test(empty(lane, s), ph)) {
-          moved = true;
-          const int tile = k < it.ns ? k : it.first + k - it.ns;
-          const bool seen = it.p1 >= 0;
-          const bool ok = seen && id >= 0 && id < a.cache.num_pages;
-          if (seen && !ok) record_index(a.err);
-          bad[lane * STAGES + s] = ok ? 0 : 1;
-          if (ok) {
-            const long long rec = ((long long)id * a.cache.Hkv + it.kvh) * tiles_per_page + tile % tiles_per_page;
-            mbar_arrive_expect_tx(full(lane, s), L::REC);
-            bulk_load(smem_u32(smem + C::SM_RING + lane * C::RING + s * L::REC),
-                      a.cache.base + rec * L::REC, L::REC, full(lane, s));
-          } else {
-            mbar_arrive(full(lane, s));
-          }
-          ++issued;
-          --left;
-          if (left > 0 && ++k == it.cnt) {
-            k = 0;
-            next_item<ROWS>(a, it);
-          }
-          id = lookup();
+      if (left > 0 && mbar_test(empty(lane, s), ph)) {
+        moved = true;
+        const bool seen = it.p1 >= 0;
+        const bool fits = seen && id >= 0 && id < a.cache.num_pages;
+        if (seen && !fits) record_index(a.err);
+        bad[lane * STAGES + s] = fits ? 0 : 1;
+        if (fits) {
+          const long long rec = ((long long)id * a.cache.Hkv + it.kvh) * a.by_page.d + rec_no - pg * a.by_page.d;
+          mbar_arrive_expect_tx(full(lane, s), L::REC);
+          bulk_load(smem_u32(smem + C::SM_RING + lane * C::RING + s * L::REC),
+                    a.cache.base + rec * L::REC, L::REC, full(lane, s));
+        } else {
+          mbar_arrive(full(lane, s));
         }
+        ++issued;
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+        --left;
+        if (left > 0 && ++k == it.cnt) {
+          k = 0;
+          next_item<ROWS>(a, it);
+        }
+        id = lookup();
       }
       if (__any_sync(0xFFFFFFFFu, moved)) {
         t0 = clock64();
-      } else if (clock64() - t0 > QK_WAIT_LIMIT_CYCLES) {
-        if (lane == 0) record_timeout(a.err);
-        break;
+      } else {
+        __nanosleep(64);  // leave the issue slots to the consumers
+        if (clock64() - t0 > QK_WAIT_LIMIT_CYCLES) {
+          if (lane == 0) record_timeout(a.err);
+          break;
+        }
       }
     }
     // every copy has landed before the block may end
@@ -451,267 +577,352 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::THREADS, 1) kv4_attn_kernel(con
     // ------------------------------------------------------------ consumers
     const int g = lane >> 2, t = lane & 3;
     const uint8_t* ring = smem + C::SM_RING + warp * C::RING;
-    const Span sp = spans[warp];
-    Item it;
-    it.b = sp.b;
-    it.rt = sp.rt;
-    it.kvh = sp.kvh;
-    int k = sp.k;
+    // this lane's places in a record: codes of tokens g, g + 8; of pairs t, t + 4
+    const uint8_t* ring_k = ring + (g * 4 + t) * 8 * NG;
+    const uint8_t* ring_v = ring + L::V_OFF + (t * 8 + g) * 8 * NG;
+    const uint8_t* ring_s = ring + L::KS_OFF + g * 4 * NG;
+    int k = sp.k, stage = 0;
+    uint32_t phase = 0;
     bool first_piece = sp.k > 0;
     int flags = 0;
     long long done = 0;
     bool ok = true;
-    if (sp.units > 0) {
-      load_request<ROWS>(a, it);
-      load_tile<ROWS>(a, it);
-    }
     while (done < sp.units && ok) {
       // ---- a segment: this span's units of one item
-      uint32_t qa[RT][NG][2][4];  // per j: the pairs (i, i + 4) of dims 64 group + 16 t + 8 j
-      float qsum[RT][NG];
-      int pos[RT];
+      // queries: fragments of row g (per j and half of a word's nibbles, the second
+      // of a pair a 16th); sums and factors of rows 2 t, 2 t + 1, the columns of the scores
+      uint32_t qb[NT][NG][2][4];
+      float qs[NT][2][NG], R[NT][2];
+      int pos[NT][2];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const int row = it.rt * ROWS + g + 8 * r;
-        const int tok = row / a.G;
+      for (int n = 0; n < NT; ++n) {
+        const int row = it.rt * ROWS + 8 * n + g;
+        const int tok = quot(row, a.by_g);
         const bool live = tok < it.n;
-        pos[r] = live ? it.len - it.n + tok : -1;
         const uint16_t* src = a.q + (long long)(it.row0 + (live ? tok : 0)) * a.q_stride +
                               (long long)(it.kvh * a.G + row - tok * a.G) * D + 16 * t;
+        uint4 raw[NG][2];
+        float top = 0.0f, sum[NG];
 #pragma unroll
         for (int grp = 0; grp < NG; ++grp) {
-          float sum = 0.0f;
+          sum[grp] = 0.0f;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (live) x = *reinterpret_cast<const uint4*>(src + 64 * grp + 8 * j);
-            qa[r][grp][j][0] = __byte_perm(x.x, x.z, 0x5410);
-            qa[r][grp][j][1] = __byte_perm(x.x, x.z, 0x7632);
-            qa[r][grp][j][2] = __byte_perm(x.y, x.w, 0x5410);
-            qa[r][grp][j][3] = __byte_perm(x.y, x.w, 0x7632);
-            const uint32_t p[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              sum += __uint_as_float(p[i] << 16) + __uint_as_float(p[i] & 0xFFFF0000u);
+            raw[grp][j] = make_uint4(0, 0, 0, 0);
+            if (live) raw[grp][j] = *reinterpret_cast<const uint4*>(src + 64 * grp + 8 * j);
           }
-          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-          qsum[r][grp] = sum;
+        }
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t w[4] = {raw[grp][j].x, raw[grp][j].y, raw[grp][j].z, raw[grp][j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              sum[grp] += bf_lo(w[i]) + bf_hi(w[i]);
+              top = fmaxf(top, fmaxf(fabsf(bf_lo(w[i])), fabsf(bf_hi(w[i]))));
+            }
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        // times 2^-e, the largest element comes into [2^13, 2^14)
+        const int e = min(max(top == 0.0f ? 0 : exponent(top) - 13, -113), 113);
+        const float f = pow2(-e);
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 v = raw[grp][j];
+            qb[n][grp][j][0] = pack_f16(bf_lo(v.x) * f, bf_lo(v.z) * f);
+            qb[n][grp][j][1] = pack_f16(bf_hi(v.x) * f * 0.0625f, bf_hi(v.z) * f * 0.0625f);
+            qb[n][grp][j][2] = pack_f16(bf_lo(v.y) * f, bf_lo(v.w) * f);
+            qb[n][grp][j][3] = pack_f16(bf_hi(v.y) * f * 0.0625f, bf_hi(v.w) * f * 0.0625f);
+          }
+          sum[grp] += __shfl_xor_sync(0xFFFFFFFFu, sum[grp], 1);
+          sum[grp] += __shfl_xor_sync(0xFFFFFFFFu, sum[grp], 2);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int from = 4 * (2 * t + c);  // a lane of row 2 t + c
+          const int ec = __shfl_sync(0xFFFFFFFFu, e, from);
+          // the scores' unit: x = 2^(24 + e) times what the codes' product gives
+          // (neither 0 nor infinite: a masked score is -inf, one of 0 stays 0)
+          R[n][c] = fminf(fmaxf(a.sc * pow2(min(24 + ec, 127)), 1.0e-35f), 3.0e38f);
+#pragma unroll
+          for (int grp = 0; grp < NG; ++grp)
+            qs[n][c][grp] = __shfl_sync(0xFFFFFFFFu, sum[grp], from) * (pow2(-ec) * 0x1p-24f);
+          const int rc = it.rt * ROWS + 8 * n + 2 * t + c;
+          const int tc = quot(rc, a.by_g);
+          pos[n][c] = tc < it.n ? it.len - it.n + tc : -1;
         }
       }
-      float m[RT], l[RT], off[RT][NG], o[NG][2][4][4];
+      // nm: minus the reference, in units of log2; lim: the score that moves it (the
+      // maximum and 2^4); o: rows g (even dims) and g + 8 (odd dims, 16-fold)
+      float nm[NT][2], lim[NT][2], l[NT][2], off[NT][2][NG], o[NT][NG][2][2][4];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        m[r] = kNone;
-        l[r] = 0.0f;
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int grp = 0; grp < NG; ++grp) off[r][grp] = 0.0f;
-      }
+        for (int c = 0; c < 2; ++c) {
+          nm[n][c] = -fmaxf(kNone * R[n][c], kLeast);
+          lim[n][c] = kNone;
+          l[n][c] = 0.0f;
 #pragma unroll
-      for (int grp = 0; grp < NG; ++grp)
+          for (int grp = 0; grp < NG; ++grp) off[n][c][grp] = 0.0f;
+        }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+        for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[grp][h][i][c] = 0.0f;
+          for (int i = 0; i < 16; ++i) o[n][grp][i >> 3][(i >> 2) & 1][i & 3] = 0.0f;
+      auto rescale = [&](int n, const float (&alpha)[2]) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          l[n][c] *= alpha[c];
+#pragma unroll
+          for (int grp = 0; grp < NG; ++grp) off[n][c][grp] *= alpha[c];
+        }
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[n][grp][i >> 3][(i >> 2) & 1][i & 3] *= alpha[i & 1];
+      };
 
       const long long room = sp.units - done;
       const int stop = (long long)(it.cnt - k) <= room ? it.cnt : k + (int)room;
       const bool ends = stop == it.cnt;
-      for (; k < stop; ++k, ++done) {
-        const int s = (int)(done % STAGES);
-        if (!mbar_wait(full(warp, s), (uint32_t)((done / STAGES) & 1), a.err)) {
+      done += stop - k;
+      for (; k < stop; ++k) {
+        const uint32_t bar = full(warp, stage);
+        if (!mbar_wait(bar, phase, a.err)) {
           ok = false;
           break;
         }
-        if (bad[warp * STAGES + s]) {  // nothing to see, or no such page
+        const int at = stage * L::REC;
+        const int is_bad = bad[warp * STAGES + stage];
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (is_bad) {  // nothing to see, or no such page
           __syncwarp();
-          if (lane == 0) mbar_arrive(empty(warp, s));
+          if (lane == 0) mbar_arrive(bar + 8u);
           continue;
         }
-        const uint8_t* rec = ring + s * L::REC;
-        const int tile = k < it.ns ? k : it.first + k - it.ns;
-        const int key0 = tile << 4;
 
-        // ---- scores of 16 keys: x[half][row][column]
-        float x[2][RT][2];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          uint32_t kw[2 * NG], ks[2 * NG];
-          lds(kw, rec + ((8 * nt + g) * 4 + t) * 8 * NG);
-          lds(ks, rec + L::KS_OFF + (8 * nt + 2 * t) * 4 * NG);
-          float acc[NG][4];
+        // ---- scores: x[n][i], i = 0, 1 key g and rows 2 t, 2 t + 1; i = 2, 3 key g + 8
+        float x[NT][4];
+        {
+          uint32_t k0[2 * NG], k1[2 * NG], s0[NG], s1[NG];
+          lds(k0, ring_k + at);
+          lds(k1, ring_k + at + 8 * 4 * 8 * NG);
+          lds(s0, ring_s + at);
+          lds(s1, ring_s + at + 8 * 4 * NG);
 #pragma unroll
           for (int grp = 0; grp < NG; ++grp) {
+            float acc[NT][4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[grp][c] = 0.0f;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+              for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
 #pragma unroll
-              for (int i = 0; i < 4; i += 2)
-                mma(acc[grp], qa[0][grp][j][i], kWide ? qa[RT - 1][grp][j][i] : 0u,
-                    qa[0][grp][j][i + 1], kWide ? qa[RT - 1][grp][j][i + 1] : 0u,
-                    code_pair(kw[2 * grp + j], i), code_pair(kw[2 * grp + j], i + 1));
-          }
+            for (int j = 0; j < 2; ++j) {
+              uint32_t u = k0[2 * grp + j], v = k1[2 * grp + j];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float v[RT];
+              for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r) v[r] = 0.0f;
-#pragma unroll
-            for (int grp = 0; grp < NG; ++grp) {
-              const float2 so = __half22float2(*reinterpret_cast<const __half2*>(&ks[c * NG + grp]));
-#pragma unroll
-              for (int r = 0; r < RT; ++r)
-                v[r] = fmaf(so.x, acc[grp][2 * r + c], fmaf(so.y, qsum[r][grp], v[r]));
-            }
-#pragma unroll
-            for (int r = 0; r < RT; ++r) x[nt][r][c] = v[r] * a.sc;
-          }
-        }
-        // ---- masks: only records that some row does not see whole
-        if (key0 + 15 > it.p0 ||
-            (a.window > 0 && key0 <= it.p1 - a.window && key0 + 15 >= a.sinks)) {
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int key = key0 + 8 * nt + 2 * t + c;
-#pragma unroll
-              for (int r = 0; r < RT; ++r) {
-                bool see = key <= pos[r];
-                if (a.window > 0) see = see && (key > pos[r] - a.window || key < a.sinks);
-                if (!see) x[nt][r][c] = -INFINITY;
+                for (int n = 0; n < NT; ++n)
+                  mma(acc[n], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
+                      qb[n][grp][j][2 * h], qb[n][grp][j][2 * h + 1]);
+                u >>= 8;
+                v >>= 8;
               }
             }
-        }
-        // ---- softmax: the reference maximum moves only by more than 2^8
-        float alpha[RT];
-        bool turn = false;
+            const float2 a0 = unpack_f16(s0[grp]), a1 = unpack_f16(s1[grp]);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          float top = fmaxf(fmaxf(x[0][r][0], x[0][r][1]), fmaxf(x[1][r][0], x[1][r][1]));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          const float to = top > m[r] + 8.0f ? top : m[r];
-          alpha[r] = ex2(m[r] - to);
-          turn |= to != m[r];
-          m[r] = to;
-        }
-        if (__any_sync(0xFFFFFFFFu, turn)) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            l[r] *= alpha[r];
-#pragma unroll
-            for (int grp = 0; grp < NG; ++grp) off[r][grp] *= alpha[r];
+              for (int c = 0; c < 2; ++c) {
+                const float z0 = a0.y * qs[n][c][grp], z1 = a1.y * qs[n][c][grp];
+                x[n][c] = fmaf(a0.x, acc[n][c], grp == 0 ? z0 : x[n][c] + z0);
+                x[n][2 + c] = fmaf(a1.x, acc[n][2 + c], grp == 0 ? z1 : x[n][2 + c] + z1);
+              }
           }
-#pragma unroll
-          for (int grp = 0; grp < NG; ++grp)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) o[grp][h][i][c] *= alpha[kWide ? c >> 1 : 0];
         }
+        const bool masked = k < it.whole0 || k >= it.whole1;
+        if (masked) {
+          const int key0 = (record_of(it, k) << 4) + g;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              x[nt][r][c] = ex2(x[nt][r][c] - m[r]);
-              l[r] += x[nt][r][c];
-            }
-        // ---- values
-        uint32_t vw[2][2 * NG], vs[2][2 * NG];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          lds(vw[nt], rec + L::V_OFF + ((4 * nt + t) * 8 + g) * 8 * NG);
-          lds(vs[nt], rec + L::VS_OFF + (8 * nt + 2 * t) * 4 * NG);
-        }
-        __syncwarp();  // every lane has read the record
-        if (lane == 0) mbar_arrive(empty(warp, s));
-#pragma unroll
-        for (int grp = 0; grp < NG; ++grp) {
-          uint32_t hi[2][RT], lo[2][RT];
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const float2 s0 = __half22float2(*reinterpret_cast<const __half2*>(&vs[nt][grp]));
-            const float2 s1 = __half22float2(*reinterpret_cast<const __half2*>(&vs[nt][NG + grp]));
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-              // a key that a row does not see has weight 0: its record may hold anything
-              const float p0 = x[nt][r][0], p1 = x[nt][r][1];
-              off[r][grp] += (p0 == 0.0f ? 0.0f : p0 * s0.y) + (p1 == 0.0f ? 0.0f : p1 * s1.y);
-              split2(p0 == 0.0f ? 0.0f : p0 * s0.x, p1 == 0.0f ? 0.0f : p1 * s1.x, &hi[nt][r],
-                     &lo[nt][r]);
-            }
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t b0 = code_pair(vw[0][2 * grp + h], i), b1 = code_pair(vw[1][2 * grp + h], i);
-              if constexpr (kWide) {
-                mma(o[grp][h][i], hi[0][0], hi[0][RT - 1], hi[1][0], hi[1][RT - 1], b0, b1);
-                mma(o[grp][h][i], lo[0][0], lo[0][RT - 1], lo[1][0], lo[1][RT - 1], b0, b1);
-              } else {
-                mma(o[grp][h][i], hi[0][0], lo[0][0], hi[1][0], lo[1][0], b0, b1);
-              }
+              const int key = key0 + 4 * (i & 2), p = pos[n][i & 1];
+              bool see = key <= p;
+              if (a.window > 0) see = see && (key > p - a.window || key < a.sinks);
+              if (!see) x[n][i] = -INFINITY;
             }
+        }
+        // ---- values and their scales; the record is free then
+        uint32_t v0[2 * NG], v1[2 * NG], t0[NG], t1[NG];
+        lds(v0, ring_v + at);
+        lds(v1, ring_v + at + 4 * 8 * 8 * NG);
+        lds(t0, ring_s + at + 16 * 4 * NG);
+        lds(t1, ring_s + at + 24 * 4 * NG);
+        __syncwarp();  // every lane has read the record
+        if (lane == 0) mbar_arrive(bar + 8u);
+        // ---- a row's reference moves only where a score passes the last maximum by 2^4
+        bool turn = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) turn |= fmaxf(x[n][c], x[n][2 + c]) > lim[n][c];
+        if (__any_sync(0xFFFFFFFFu, turn)) {
+          const float m0 = largest_scale(t0), m1 = largest_scale(t1);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float alpha[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float top = column_max(fmaxf(x[n][c], x[n][2 + c]));
+              const float heavy = column_max(fmaxf(ex2((x[n][c] - top) * R[n][c]) * m0,
+                                                   ex2((x[n][2 + c] - top) * R[n][c]) * m1));
+              const float was = nm[n][c];
+              if (top > lim[n][c]) {
+                nm[n][c] = (float)(9 - exponent(fmaxf(heavy, 0x1p-24f))) - fmaxf(top * R[n][c], kLeast);
+                lim[n][c] = top + 4.0f / R[n][c];
+              }
+              alpha[c] = ex2(nm[n][c] - was);
+            }
+            rescale(n, alpha);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[n][i] = ex2(fmaf(x[n][i], R[n][i & 1], nm[n][i & 1]));
+        // ---- weights times scales, as the second product's operand
+        uint32_t w[NT][NG][2];
+        auto weights = [&]() {
+          uint32_t big = 0;
+#pragma unroll
+          for (int grp = 0; grp < NG; ++grp) {
+            const float s0 = unpack_f16(t0[grp]).x, s1 = unpack_f16(t1[grp]).x;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (masked)
+                weigh<true>(x[n], s0, s1, w[n][grp]);
+              else
+                weigh<false>(x[n], s0, s1, w[n][grp]);
+              big = __vmaxu2(big, __vmaxu2(w[n][grp][0], w[n][grp][1]));
+            }
+          }
+          return big;
+        };
+        // a half of 2^15 or more carries into its sign bit
+        if (__any_sync(0xFFFFFFFFu, ((weights() + 0x08000800u) & 0x80008000u) != 0)) {
+          const float m0 = largest_scale(t0), m1 = largest_scale(t1);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float alpha[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float heavy = column_max(fmaxf(x[n][c] * m0, x[n][2 + c] * m1));
+              const float was = nm[n][c];
+              if (heavy >= 0x1p14f) nm[n][c] -= (float)(exponent(heavy) - 9);
+              alpha[c] = ex2(nm[n][c] - was);
+              x[n][c] *= alpha[c];
+              x[n][2 + c] *= alpha[c];
+            }
+            rescale(n, alpha);
+          }
+          weights();
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          l[n][0] += x[n][0] + x[n][2];
+          l[n][1] += x[n][1] + x[n][3];
+        }
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) {
+          const float o0 = unpack_f16(t0[grp]).y, o1 = unpack_f16(t1[grp]).y;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (masked)
+                off[n][c][grp] += (x[n][c] == 0.0f ? 0.0f : x[n][c] * o0) +
+                                  (x[n][2 + c] == 0.0f ? 0.0f : x[n][2 + c] * o1);
+              else
+                off[n][c][grp] = fmaf(x[n][c], o0, fmaf(x[n][2 + c], o1, off[n][c][grp]));
+            }
+        }
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            w[n][grp][0] = transpose8(w[n][grp][0]);
+            w[n][grp][1] = transpose8(w[n][grp][1]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t u = v0[2 * grp + h], v = v1[2 * grp + h];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma(o[n][grp][h][i], u & 0x000F000Fu, u & 0x00F000F0u, v & 0x000F000Fu,
+                    v & 0x00F000F0u, w[n][grp][0], w[n][grp][1]);
+              u >>= 8;
+              v >>= 8;
+            }
+          }
         }
       }
       if (!ok) break;
 
-      // ---- the segment's sums: l, the offsets' part, and the low halves' rows
+      // ---- the segment's sums: l and the offsets' part over the lanes of a row; then
+      // z = O of row 2 t + c, dims 64 group + 8 g + 4 h + 2 i + (0, 1)
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int grp = 0; grp < NG; ++grp) {
-          off[r][grp] += __shfl_xor_sync(0xFFFFFFFFu, off[r][grp], 1);
-          off[r][grp] += __shfl_xor_sync(0xFFFFFFFFu, off[r][grp], 2);
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], d);
+#pragma unroll
+            for (int grp = 0; grp < NG; ++grp)
+              off[n][c][grp] += __shfl_xor_sync(0xFFFFFFFFu, off[n][c][grp], d);
+          }
         }
-      }
 #pragma unroll
-      for (int grp = 0; grp < NG; ++grp)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float* v = o[grp][h][i];
-            if constexpr (kWide) {
-              v[0] += off[0][grp]; v[1] += off[0][grp];
-              v[2] += off[RT - 1][grp]; v[3] += off[RT - 1][grp];
-            } else {
-              v[0] += v[2] + off[0][grp];
-              v[1] += v[3] + off[0][grp];
-            }
+          for (int i = 0; i < 16; ++i) {
+            float& z = o[n][grp][i >> 3][(i >> 2) & 1][i & 3];
+            z = fmaf(z, (i & 2) ? 0x1p20f : 0x1p24f, off[n][i & 1][grp]);
           }
       if (ends && !first_piece) {
-        // the whole item: dims 64 group + 16 t + 8 c + 4 h + i of row g (+ 8)
+        // the whole item
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const int row = it.rt * ROWS + g + 8 * r;
-          const int tok = row / a.G;
-          if (tok >= it.n) continue;
-          const float inv = l[r] > 0.0f ? 1.0f / l[r] : (l[r] == 0.0f ? 0.0f : l[r]);
-          uint16_t* dst = a.out + ((long long)(it.row0 + tok) * a.H + it.kvh * a.G + row - tok * a.G) * D + 16 * t;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int grp = 0; grp < NG; ++grp)
+          for (int c = 0; c < 2; ++c) {
+            const int row = it.rt * ROWS + 8 * n + 2 * t + c;
+            const int tok = quot(row, a.by_g);
+            if (tok >= it.n) continue;
+            const float inv = l[n][c] > 0.0f ? 1.0f / l[n][c] : l[n][c];  // (0, or NaN)
+            uint16_t* dst = a.out + ((long long)(it.row0 + tok) * a.H + it.kvh * a.G + row - tok * a.G) * D + 8 * g;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t w[4];
+            for (int grp = 0; grp < NG; ++grp) {
+              uint32_t y[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack16(o[grp][e >> 1][2 * (e & 1)][2 * r + c] * inv,
-                              o[grp][e >> 1][2 * (e & 1) + 1][2 * r + c] * inv);
-              *reinterpret_cast<uint4*>(dst + 64 * grp + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int i = 0; i < 4; ++i)
+                y[i] = pack_bf16(o[n][grp][i >> 1][i & 1][c] * inv, o[n][grp][i >> 1][i & 1][2 + c] * inv);
+              *reinterpret_cast<uint4*>(dst + 64 * grp) = make_uint4(y[0], y[1], y[2], y[3]);
             }
-        }
+          }
       } else {
         // a piece: an item's end or middle goes to the head slot, its beginning to the ring
         // (whose copies have all been read: this is the span's last segment)
@@ -719,27 +930,30 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::THREADS, 1) kv4_attn_kernel(con
                                                             : smem + C::SM_RING + warp * C::RING);
         __syncwarp();
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          float* dst = piece + (g + 8 * r) * C::LD + 16 * t;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int grp = 0; grp < NG; ++grp)
+          for (int c = 0; c < 2; ++c) {
+            const int row = 8 * n + 2 * t + c;
+            float* dst = piece + row * C::LD + 8 * g;
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<float4*>(dst + 64 * grp + 8 * c + 4 * h) =
-                    make_float4(o[grp][h][0][2 * r + c], o[grp][h][1][2 * r + c],
-                                o[grp][h][2][2 * r + c], o[grp][h][3][2 * r + c]);
-          if (t == 0) {
-            piece[ROWS * C::LD + g + 8 * r] = m[r];
-            piece[ROWS * C::LD + ROWS + g + 8 * r] = l[r];
+                *reinterpret_cast<float4*>(dst + 64 * grp + 4 * h) =
+                    make_float4(o[n][grp][h][0][c], o[n][grp][h][0][2 + c], o[n][grp][h][1][c],
+                                o[n][grp][h][1][2 + c]);
+            if (g == 0) {
+              piece[ROWS * C::LD + row] = -nm[n][c];
+              piece[ROWS * C::LD + ROWS + row] = l[n][c];
+            }
           }
-        }
-        if (lane == 0) {
-          int* id = seg_item[warp] + (first_piece ? 0 : 3);
+        if (lane == 0 && !first_piece) {
+          int* id = seg_item[warp];
           id[0] = it.b;
           id[1] = it.rt;
           id[2] = it.kvh;
+          id[3] = it.row0;
+          id[4] = it.n;
         }
         flags |= first_piece ? (ends ? 3 : 1) : 4;
       }
@@ -753,58 +967,61 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::THREADS, 1) kv4_attn_kernel(con
   }
   __syncthreads();
 
-  // ---- join the pieces that meet in this block
+  // ---- join the pieces that meet in this block: a chain is a last piece (in its
+  // warp's ring), if it began here, and the first pieces of the warps behind it
+  const int my_flags = seg_flags[lane];
+  const uint32_t heads = __ballot_sync(0xFFFFFFFFu, my_flags & 1);
+  const uint32_t end_at = __ballot_sync(0xFFFFFFFFu, my_flags & 2);
+  const uint32_t tails = __ballot_sync(0xFFFFFFFFu, my_flags & 4);
   Meta meta = {0, 0, 0, 0};
-  int start = -1;       // warp whose last piece began the chain; -2: it began in an earlier block
-  int from = 0;         // first head piece of the chain
-  auto emit = [&](int last, bool ended) {
-    // pieces: start's ring (where start >= 0), then the heads of warps from .. last
-    const int* id = start >= 0 ? seg_item[start] + 3 : seg_item[from];
-    const int b = id[0], rt = id[1], kvh = id[2];
+  auto emit = [&](int start, uint32_t parts, bool ended) {
     const bool whole = start >= 0 && ended;
     float* part = nullptr;
     if (!whole) {
       part = piece_at(a.ws, D, blk, start >= 0 ? 1 : 0);
       if (start >= 0) {
         meta.flags |= 4;
-        meta.b = b;
-        meta.rt = rt;
-        meta.kvh = kvh;
+        meta.b = seg_item[start][0];
+        meta.rt = seg_item[start][1];
+        meta.kvh = seg_item[start][2];
       } else {
         meta.flags |= ended ? 3 : 1;
       }
     }
-    Kv4Seq sq = {};
-    if (whole) sq = kv4_seq(a.req, b, a.err);
-    auto piece = [&](int w) {
-      return reinterpret_cast<const float*>(w < from ? smem + C::SM_RING + start * C::RING
-                                                     : smem + C::SM_HEAD + w * C::PIECE);
-    };
-    const int w0 = start >= 0 ? from - 1 : from;
+    const float* first = reinterpret_cast<const float*>(smem + C::SM_RING + max(start, 0) * C::RING);
+    const float* rest = reinterpret_cast<const float*>(smem + C::SM_HEAD);
     for (int e = threadIdx.x; e < ROWS * (D / 4); e += C::THREADS) {
       const int r = e / (D / 4), d = 4 * (e % (D / 4));
-      float top = kNone;
-      for (int w = w0; w <= last; ++w)
-        if (w < from || (seg_flags[w] & 1)) top = fmaxf(top, piece(w)[ROWS * C::LD + r]);
+      // weights of all pieces first, so that their loads do not wait for one another
+      float wt[NW], own = kLeast, top = kLeast;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        wt[w] = (parts >> w) & 1u ? rest[w * (C::PIECE / 4) + ROWS * C::LD + r] : kLeast;
+        top = fmaxf(top, wt[w]);
+      }
+      if (start >= 0) own = first[ROWS * C::LD + r];
+      top = fmaxf(top, own);
       float sum = 0.0f;
       float4 v = make_float4(0, 0, 0, 0);
-      for (int w = w0; w <= last; ++w) {
-        if (w >= from && !(seg_flags[w] & 1)) continue;
-        const float* p = piece(w);
-        const float f = ex2(p[ROWS * C::LD + r] - top);
+      auto add = [&](const float* p, float f) {
         sum = fmaf(f, p[ROWS * C::LD + ROWS + r], sum);
         const float4 x = *reinterpret_cast<const float4*>(p + r * C::LD + d);
         v.x = fmaf(f, x.x, v.x);
         v.y = fmaf(f, x.y, v.y);
         v.z = fmaf(f, x.z, v.z);
         v.w = fmaf(f, x.w, v.w);
-      }
+      };
+      if (start >= 0) add(first, ex2(own - top));
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+        if ((parts >> w) & 1u) add(rest + w * (C::PIECE / 4), ex2(wt[w] - top));
       if (whole) {
-        const int row = rt * ROWS + r, tok = row / a.G;
-        if (tok < sq.n) {
-          const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-          uint16_t* dst = a.out + ((long long)(sq.row0 + tok) * a.H + kvh * a.G + row - tok * a.G) * D + d;
-          *reinterpret_cast<uint2*>(dst) = make_uint2(pack16(v.x * inv, v.y * inv), pack16(v.z * inv, v.w * inv));
+        const int row = seg_item[start][1] * ROWS + r, tok = quot(row, a.by_g);
+        if (tok < seg_item[start][4]) {
+          const float inv = sum > 0.0f ? 1.0f / sum : sum;
+          uint16_t* dst = a.out + ((long long)(seg_item[start][3] + tok) * a.H + seg_item[start][2] * a.G +
+                                   row - tok * a.G) * D + d;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
         }
       } else {
         *reinterpret_cast<float4*>(part + r * D + d) = v;
@@ -815,71 +1032,118 @@ __global__ void __launch_bounds__(Cfg<D, kWide>::THREADS, 1) kv4_attn_kernel(con
       }
     }
   };
+  int start = -1;       // the chain's last piece; -1: it began in an earlier block
+  uint32_t parts = 0;   // its first pieces
+  bool open = heads != 0 && (tails & ((heads & (0u - heads)) - 1u)) == 0;
   for (int w = 0; w < NW; ++w) {
-    const int f = seg_flags[w];
-    if (f & 1) {
-      if (start == -1) {
-        start = -2;
-        from = w;
-      }
-      if (f & 2) {
-        emit(w, true);
-        start = -1;
+    if ((heads >> w) & 1u) {
+      parts |= 1u << w;
+      if ((end_at >> w) & 1u) {
+        if (open) emit(start, parts, true);
+        open = false;
+        parts = 0;
       }
     }
-    if (f & 4) {
+    if ((tails >> w) & 1u) {
       start = w;
-      from = w + 1;
+      parts = 0;
+      open = true;
     }
   }
-  if (start != -1) emit(NW - 1, false);
+  if (open) emit(start, parts, false);
   if (threadIdx.x == 0) reinterpret_cast<Meta*>(a.ws + kMetaOff)[blk] = meta;
 }
 
 // Joins the items that are cut between blocks: block (c, row) the one whose
 // beginning is block c's last piece, with the first pieces of the blocks behind it.
+// D / 4 threads read a piece's row; the 512 / D groups of them take the pieces in turn.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(D) kv4_join_kernel(const Args a) {
+__global__ void __launch_bounds__(128) kv4_join_kernel(const Args a) {
+  constexpr int TPP = D / 4, GROUPS = 128 / TPP;
+  __shared__ float weight[kMaxBlocks + 1];
+  __shared__ __align__(16) float red[GROUPS][D];
+  __shared__ float total;
   pdl_launch_dependents();
   pdl_wait();
-  const int c = blockIdx.x, r = blockIdx.y, d = threadIdx.x;
+  const int c = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31;
   const int blocks = *reinterpret_cast<const int*>(a.ws);
-  if (c >= blocks) return;
   const Meta* meta = reinterpret_cast<const Meta*>(a.ws + kMetaOff);
+  if (c >= blocks) return;
   const Meta me = meta[c];
   if (!(me.flags & 4)) return;
-  const Kv4Seq sq = kv4_seq(a.req, me.b, a.err);
-  const int row = me.rt * ROWS + r, tok = row / a.G;
-  if (tok >= sq.n) return;
-  const float* p = piece_at(a.ws, D, c, 1);
-  float top = p[16 * D + r], sum = p[16 * D + 16 + r], v = p[r * D + d];
-  for (int e = c + 1; e < blocks; ++e) {
-    const int f = meta[e].flags;
-    if (!(f & 1)) continue;
-    const float* x = piece_at(a.ws, D, e, 0);
-    const float xm = x[16 * D + r];
-    const float to = fmaxf(top, xm);
-    const float fa = ex2(top - to), fb = ex2(xm - to);
-    sum = fa * sum + fb * x[16 * D + 16 + r];
-    v = fa * v + fb * x[r * D + d];
-    top = to;
-    if (f & 2) break;
+  // the chain: blocks c + 1 .. last (a block with no first piece in it has no units)
+  int last = blocks - 1;
+  for (int e0 = c + 1; e0 < blocks; e0 += 32) {
+    const int e = e0 + lane;
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, e < blocks && (meta[e].flags & 2) != 0);
+    if (hit != 0) {
+      last = e0 + __ffs(hit) - 1;
+      break;
+    }
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-  const __nv_bfloat16 y = __float2bfloat16_rn(v * inv);
-  a.out[((long long)(sq.row0 + tok) * a.H + me.kvh * a.G + row - tok * a.G) * D + d] =
-      *reinterpret_cast<const uint16_t*>(&y);
+  const int n = last - c + 1;
+  auto piece = [&](int i) { return piece_at(a.ws, D, c + i, i == 0 ? 1 : 0); };
+  if (threadIdx.x < 32) {
+    float top = kLeast;
+    for (int i = lane; i < n; i += 32) {
+      const bool has = i == 0 || (meta[c + i].flags & 1) != 0;
+      const float m = has ? piece(i)[16 * D + r] : kLeast;
+      weight[i] = has ? m : -INFINITY;
+      top = fmaxf(top, m);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    float sum = 0.0f;
+    for (int i = lane; i < n; i += 32) {
+      const float f = ex2(weight[i] - top);
+      weight[i] = f;
+      if (f != 0.0f) sum = fmaf(f, piece(i)[16 * D + 16 + r], sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) total = sum;
+  }
+  __syncthreads();
+  const int grp = threadIdx.x / TPP, d = 4 * (threadIdx.x % TPP);
+  float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int i = grp; i < n; i += GROUPS) {
+    const float f = weight[i];
+    if (f == 0.0f) continue;
+    const float4 x = *reinterpret_cast<const float4*>(piece(i) + r * D + d);
+    v.x = fmaf(f, x.x, v.x);
+    v.y = fmaf(f, x.y, v.y);
+    v.z = fmaf(f, x.z, v.z);
+    v.w = fmaf(f, x.w, v.w);
+  }
+  *reinterpret_cast<float4*>(&red[grp][d]) = v;
+  __syncthreads();
+  if (threadIdx.x >= TPP) return;
+#pragma unroll
+  for (int i = 1; i < GROUPS; ++i) {
+    const float4 x = *reinterpret_cast<const float4*>(&red[i][d]);
+    v.x += x.x;
+    v.y += x.y;
+    v.z += x.z;
+    v.w += x.w;
+  }
+  const Kv4Seq sq = kv4_seq(a.req, me.b, a.err);
+  const int row = me.rt * ROWS + r, tok = quot(row, a.by_g);
+  if (tok >= sq.n) return;
+  const float sum = total, inv = sum > 0.0f ? 1.0f / sum : sum;
+  uint16_t* dst = a.out + ((long long)(sq.row0 + tok) * a.H + me.kvh * a.G + row - tok * a.G) * D + d;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
 }
 
-template <int D, bool kWide>
+template <int D, int NT>
 cudaError_t launch(const Args& a, cudaStream_t s) {
-  using C = Cfg<D, kWide>;
+  using C = Cfg<D, NT>;
   static bool done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && !done[dev]) {
-    e = cudaFuncSetAttribute(kv4_attn_kernel<D, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::SMEM);
     if (e != cudaSuccess) return e;
     done[dev] = true;
@@ -895,10 +1159,10 @@ cudaError_t launch(const Args& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv4_attn_kernel<D, kWide>, a, 2);
+  e = cudaLaunchKernelEx(&cfg, kv4_attn_kernel<D, NT>, a, 2);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)blocks, C::ROWS);
-  cfg.blockDim = dim3(D);
+  cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, C::ROWS>, a);
 }
@@ -917,6 +1181,8 @@ cudaError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t H,
   a.q_stride = q_stride;
   a.H = (int)H;
   a.G = (int)(H / cache.Hkv);
+  a.by_g = fast_div(a.G);
+  a.by_page = fast_div(cache.page / 16);
   a.req = req;
   a.cache = cache;
   a.sc = scale * 1.4426950408889634f;
@@ -925,11 +1191,11 @@ cudaError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t H,
   a.out = out;
   a.ws = static_cast<uint8_t*>(workspace);
   a.err = err;
-  // rows of a request's tile: 8 where the batch's average request has no more
+  // rows of an item: 8 where the batch's average request has no more
   const int64_t rows = a.G * ((req.T + req.B - 1) / req.B);
   const bool wide = rows > 8;
-  if (cache.D == 64) return wide ? launch<64, true>(a, s) : launch<64, false>(a, s);
-  return wide ? launch<128, true>(a, s) : launch<128, false>(a, s);
+  if (cache.D == 64) return wide ? launch<64, 2>(a, s) : launch<64, 1>(a, s);
+  return wide ? launch<128, 2>(a, s) : launch<128, 1>(a, s);
 }
 
 }  // namespace qk

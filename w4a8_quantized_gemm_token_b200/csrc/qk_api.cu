@@ -817,7 +817,7 @@ qk_status qk_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64
   qk_status st =
       kv4_check(T, Hkv, D, page_table, B, max_pages, kv_lens, cu_rows, cache, num_pages, page);
   if (st != QK_OK) return st;
-  if (H < 1 || H > INT32_MAX || H % Hkv != 0 || H / Hkv * T > INT32_MAX ||
+  if (H < 1 || H > INT32_MAX || H % Hkv != 0 || H / Hkv * T > (int64_t(1) << 30) ||
       window > (int64_t(1) << 30) || sinks > (int64_t(1) << 30) || q_stride < H * D ||
       q_stride % 8 != 0)
     return QK_ERR_UNSUPPORTED_SHAPE;
