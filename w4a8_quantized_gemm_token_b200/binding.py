@@ -123,7 +123,8 @@ def _check(status: int, where: str) -> None:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: a torch.cuda.Stream object costs 3 us, this 0.2
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -447,12 +448,13 @@ def qk_sage_attention(q, k, v, scale=None, out=None, workspace=None, stream=None
 
 # ---------------------------------------- norm, rotary positions, 4-bit cache
 
-def _same_device(**tensors) -> None:
-    """Every tensor on the current CUDA device, where the kernels launch."""
+def _same_device(*tensors) -> None:
+    """Every tensor (or None) on the current CUDA device, where the kernels launch."""
     here = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != here:
-            raise ValueError(f"{name} is on {t.device}, and the current device is cuda:{here}")
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, and the current "
+                             f"device is cuda:{here}")
 
 
 def _rows(t, heads, D, name):
@@ -462,15 +464,23 @@ def _rows(t, heads, D, name):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, D):
+    if t.dim() != 3 or t.shape[1:] != (heads, D):
         raise ValueError(f"{name} must have shape [T, {heads}, {D}], got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.shape[0] == 0:
+    T = t.shape[0]
+    if T == 0:
         return heads * D
-    if (D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D):
+    row, head, one = t.stride()
+    if (D > 1 and one != 1) or (heads > 1 and head != D):
         raise ValueError(f"{name}: a row's heads must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(heads * D, t.stride(0))
+    return row if T > 1 else max(heads * D, row)
+
+
+def _new_rows(like, T, heads, D):
+    """An empty contiguous bf16 [T, heads, D] beside `like`."""
+    return torch.empty_strided((T, heads, D), (heads * D, D, 1), dtype=torch.bfloat16,
+                               device=like.device)
 
 
 def qk_rmsnorm_quantize(x, weight=None, residual=None, eps=1e-6, h=None, xq=None, sx=None,
@@ -489,16 +499,26 @@ def qk_rmsnorm_quantize(x, weight=None, residual=None, eps=1e-6, h=None, xq=None
         _need(residual, torch.bfloat16, 2, "residual")
         if residual.shape != x.shape:
             raise ValueError("residual must have x's shape")
-        h = _out(h, (M, K), torch.bfloat16, x.device, "h")
+        # (empty_like and empty_strided: half the time of torch.empty)
+        h = torch.empty_like(x) if h is None else _out(h, (M, K), torch.bfloat16, x.device, "h")
     elif h is not None:
         raise ValueError("h is written with a residual only")
-    xq = _out(xq, (M, K), torch.int8, x.device, "xq")
-    sx = _out(sx, (M,), torch.float32, x.device, "sx")
-    if with_xsum or xsum is not None:
-        xsum = _out(xsum, (M, K // 64), torch.int32, x.device, "xsum")
-    _same_device(x=x, weight=weight, residual=residual, h=h, xq=xq, sx=sx, xsum=xsum)
-    _check(lib.qk_rmsnorm_quantize(_ptr(x), _ptr(residual), M, K, _ptr(weight), float(eps), _ptr(h),
-                                   _ptr(xq), _ptr(sx), _ptr(xsum), _stream(stream)),
+    dev = x.device
+    if xq is None:
+        xq = torch.empty_strided((M, K), (K, 1), dtype=torch.int8, device=dev)
+    else:
+        _out(xq, (M, K), torch.int8, dev, "xq")
+    if sx is None:
+        sx = torch.empty_strided((M,), (1,), dtype=torch.float32, device=dev)
+    else:
+        _out(sx, (M,), torch.float32, dev, "sx")
+    if xsum is not None:
+        _out(xsum, (M, K // 64), torch.int32, dev, "xsum")
+    elif with_xsum:
+        xsum = torch.empty_strided((M, K // 64), (max(1, K // 64), 1), dtype=torch.int32, device=dev)
+    _same_device(x, weight, residual, h, xq, sx, xsum)
+    _check(lib.qk_rmsnorm_quantize(x.data_ptr(), _ptr(residual), M, K, _ptr(weight), eps, _ptr(h),
+                                   xq.data_ptr(), sx.data_ptr(), _ptr(xsum), _stream(stream)),
            "qk_rmsnorm_quantize")
     return h, xq, sx, xsum
 
@@ -512,7 +532,7 @@ def qk_rope_frequencies(rot, base=10000.0, scaling=QK_ROPE_PLAIN, factor=1.0, tr
         _need(freq, torch.float64, 1, "freq")
         if freq.shape[0] != rot // 2:
             raise ValueError(f"freq must have shape [{rot // 2}]")
-    _same_device(freq=freq)
+    _same_device(freq)
     _check(lib.qk_rope_frequencies(int(rot), float(base), int(scaling), float(factor),
                                    float(trained), float(slow), float(fast), _ptr(freq),
                                    _stream(stream)), "qk_rope_frequencies")
@@ -533,8 +553,9 @@ def qk_rope(q, k, positions, freq, layout=QK_ROPE_HALF, amplitude=1.0, q_out=Non
     if positions.shape[0] != T:
         raise ValueError(f"positions must have shape [{T}]")
     if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
-    qos = _rows(q_out, H, D, "q_out")
+        q_out, qos = _new_rows(q, T, H, D), H * D
+    else:
+        qos = _rows(q_out, H, D, "q_out")
     Hkv = ks = kos = 0
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 3:
@@ -542,16 +563,17 @@ def qk_rope(q, k, positions, freq, layout=QK_ROPE_HALF, amplitude=1.0, q_out=Non
         Hkv = k.shape[1]
         ks = _rows(k, Hkv, D, "k")
         if k_out is None:
-            k_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=k.device)
-        kos = _rows(k_out, Hkv, D, "k_out")
+            k_out, kos = _new_rows(k, k.shape[0], Hkv, D), Hkv * D
+        else:
+            kos = _rows(k_out, Hkv, D, "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    if any(t is not None and t.shape[0] != T for t in (k, q_out, k_out)):
+    if q_out.shape[0] != T or (k is not None and (k.shape[0] != T or k_out.shape[0] != T)):
         raise ValueError("q, k and the outputs must have the same number of rows")
-    _same_device(q=q, k=k, positions=positions, freq=freq, q_out=q_out, k_out=k_out)
-    _check(lib.qk_rope(_ptr(q), qs, _ptr(q_out), qos, H, _ptr(k), ks, _ptr(k_out), kos, Hkv, T, D,
-                       2 * freq.shape[0], int(layout), _ptr(positions), _ptr(freq),
-                       float(amplitude), _stream(stream)), "qk_rope")
+    _same_device(q, k, positions, freq, q_out, k_out)
+    _check(lib.qk_rope(q.data_ptr(), qs, q_out.data_ptr(), qos, H, _ptr(k), ks, _ptr(k_out), kos, Hkv,
+                       T, D, 2 * freq.shape[0], int(layout), positions.data_ptr(), freq.data_ptr(),
+                       amplitude, _stream(stream)), "qk_rope")
     return q_out, k_out
 
 
@@ -560,7 +582,13 @@ def qk_kv4_cache_size(num_pages: int, Hkv: int, page: int, D: int) -> int:
 
 
 def qk_kv4_attention_workspace_size(D: int) -> int:
-    return int(lib.qk_kv4_attention_workspace_size(int(D)))
+    size = _kv4_workspace.get(D)
+    if size is None:
+        size = _kv4_workspace[D] = int(lib.qk_kv4_attention_workspace_size(int(D)))
+    return size
+
+
+_kv4_workspace = {}  # bytes by head dim
 
 
 def _kv4(cache, page_table, kv_lens, cu_rows, T):
@@ -581,7 +609,6 @@ def _kv4(cache, page_table, kv_lens, cu_rows, T):
             raise ValueError(f"cu_rows must have shape [{B + 1}]")
     elif B == 0 or T % B != 0:
         raise ValueError("without cu_rows every request has the same number of rows")
-    _same_device(cache=cache, page_table=page_table, kv_lens=kv_lens, cu_rows=cu_rows)
     return Hkv, width // 9 * 8, B, max_pages, num_pages, page
 
 
@@ -594,7 +621,7 @@ def qk_kv4_append(k, v, cache, page_table, kv_lens, cu_rows=None, stream=None):
     ks, vs = _rows(k, Hkv, D, "k"), _rows(v, Hkv, D, "v")
     if v.shape[0] != T:
         raise ValueError("k and v must have the same number of rows")
-    _same_device(k=k, v=v)
+    _same_device(k, v, cache, page_table, kv_lens, cu_rows)
     _check(lib.qk_kv4_append(_ptr(k), ks, _ptr(v), vs, T, Hkv, D, _ptr(page_table), B, max_pages,
                              _ptr(kv_lens), _ptr(cu_rows), _ptr(cache), num_pages, page,
                              _stream(stream)), "qk_kv4_append")
@@ -605,14 +632,18 @@ def qk_kv4_gather(cache, page_table, kv_lens, cu_rows, T, k=None, v=None, stream
     qk_kv4_append; all of them where a request's rows number its length)."""
     T = int(T)
     Hkv, D, B, max_pages, num_pages, page = _kv4(cache, page_table, kv_lens, cu_rows, T)
+    ks = vs = Hkv * D
     if k is None:
-        k = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=cache.device)
+        k = _new_rows(cache, T, Hkv, D)
+    else:
+        ks = _rows(k, Hkv, D, "k")
     if v is None:
-        v = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=cache.device)
-    ks, vs = _rows(k, Hkv, D, "k"), _rows(v, Hkv, D, "v")
+        v = _new_rows(cache, T, Hkv, D)
+    else:
+        vs = _rows(v, Hkv, D, "v")
     if k.shape[0] != T or v.shape[0] != T:
         raise ValueError(f"k and v must have {T} rows")
-    _same_device(k=k, v=v)
+    _same_device(k, v, cache, page_table, kv_lens, cu_rows)
     _check(lib.qk_kv4_gather(_ptr(cache), num_pages, page, Hkv, D, _ptr(page_table), B, max_pages,
                              _ptr(kv_lens), _ptr(cu_rows), T, _ptr(k), ks, _ptr(v), vs,
                              _stream(stream)), "qk_kv4_gather")
@@ -630,17 +661,20 @@ def qk_kv4_attention(q, cache, page_table, kv_lens, cu_rows=None, scale=None, wi
     T, H = q.shape[0], q.shape[1]
     Hkv, D, B, max_pages, num_pages, page = _kv4(cache, page_table, kv_lens, cu_rows, T)
     qs = _rows(q, H, D, "q")
-    out = _out(out, (T, H, D), torch.bfloat16, q.device, "out")
+    out = _new_rows(q, T, H, D) if out is None else _out(out, (T, H, D), torch.bfloat16, q.device, "out")
     s = _stream(stream)
-    if workspace is None and s == torch.cuda.current_stream().cuda_stream:
-        workspace = torch.empty(max(1, lib.qk_kv4_attention_workspace_size(D)), dtype=torch.uint8,
-                                device=q.device)
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    else:
+        ws_bytes = 0
+        if stream is None or s == _stream(None):
+            ws_bytes = qk_kv4_attention_workspace_size(D)
+            workspace = torch.empty_strided((ws_bytes,), (1,), dtype=torch.uint8, device=q.device)
     if scale is None:
         scale = D ** -0.5
-    _same_device(q=q, out=out, workspace=workspace)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib.qk_kv4_attention(_ptr(q), qs, T, H, Hkv, D, _ptr(cache), num_pages, page,
-                                _ptr(page_table), B, max_pages, _ptr(kv_lens), _ptr(cu_rows),
-                                float(scale), int(window), int(sinks), _ptr(out), _ptr(workspace),
+    _same_device(q, out, workspace, cache, page_table, kv_lens, cu_rows)
+    _check(lib.qk_kv4_attention(q.data_ptr(), qs, T, H, Hkv, D, cache.data_ptr(), num_pages, page,
+                                page_table.data_ptr(), B, max_pages, kv_lens.data_ptr(), _ptr(cu_rows),
+                                scale, int(window), int(sinks), _ptr(out), _ptr(workspace),
                                 ws_bytes, s), "qk_kv4_attention")
     return out
