@@ -5,7 +5,9 @@ contiguity, allocates outputs with ``torch.empty`` when the caller passes none,
 and forwards raw device pointers plus the current torch stream to the C call.
 Every step of the computation runs in the library's CUDA kernels; there is no
 CPU fallback.  A non-zero status raises :class:`QKError`.  If the library has
-not been built, importing this module raises.
+not been built, importing this module raises.  The calls that a decode step makes
+between its products are marshalled in C++ (csrc/block_calls.cpp), with the same
+checks and exceptions: their kernels are shorter than the checks in Python.
 """
 from __future__ import annotations
 
@@ -21,6 +23,7 @@ if not os.path.exists(_LIB_PATH):
         "(the quantized linear has no CPU fallback)")
 
 lib = ctypes.CDLL(_LIB_PATH)
+from . import _block_calls  # noqa: E402  (built beside libqk.so, and linked to it)
 
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _F, _D = ctypes.c_float, ctypes.c_double
@@ -448,39 +451,8 @@ def qk_sage_attention(q, k, v, scale=None, out=None, workspace=None, stream=None
 
 # ---------------------------------------- norm, rotary positions, 4-bit cache
 
-def _same_device(*tensors) -> None:
-    """Every tensor (or None) on the current CUDA device, where the kernels launch."""
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, and the current "
-                             f"device is cuda:{here}")
-
-
-def _rows(t, heads, D, name):
-    """A bf16 [T, heads, D] view whose heads lie next to each other (rows of a
-    larger projection may lie further apart); returns its row stride in elements."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1:] != (heads, D):
-        raise ValueError(f"{name} must have shape [T, {heads}, {D}], got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    T = t.shape[0]
-    if T == 0:
-        return heads * D
-    row, head, one = t.stride()
-    if (D > 1 and one != 1) or (heads > 1 and head != D):
-        raise ValueError(f"{name}: a row's heads must be contiguous")
-    return row if T > 1 else max(heads * D, row)
-
-
-def _new_rows(like, T, heads, D):
-    """An empty contiguous bf16 [T, heads, D] beside `like`."""
-    return torch.empty_strided((T, heads, D), (heads * D, D, 1), dtype=torch.bfloat16,
-                               device=like.device)
+def _handle(stream):
+    return None if stream is None else _stream(stream)
 
 
 def qk_rmsnorm_quantize(x, weight=None, residual=None, eps=1e-6, h=None, xq=None, sx=None,
@@ -489,38 +461,8 @@ def qk_rmsnorm_quantize(x, weight=None, residual=None, eps=1e-6, h=None, xq=None
     None): the RMS norm of h = x + residual times weight (fp32 [K]) as codes and scales, for
     qk_w8a8_gemm and qk_w4a8_gemm.  h (bf16) is the new residual stream, None without a residual;
     h may be x or residual itself."""
-    _need(x, torch.bfloat16, 2, "x")
-    M, K = x.shape
-    if weight is not None:
-        _need(weight, torch.float32, 1, "weight")
-        if weight.shape[0] != K:
-            raise ValueError(f"weight must have shape [{K}]")
-    if residual is not None:
-        _need(residual, torch.bfloat16, 2, "residual")
-        if residual.shape != x.shape:
-            raise ValueError("residual must have x's shape")
-        # (empty_like and empty_strided: half the time of torch.empty)
-        h = torch.empty_like(x) if h is None else _out(h, (M, K), torch.bfloat16, x.device, "h")
-    elif h is not None:
-        raise ValueError("h is written with a residual only")
-    dev = x.device
-    if xq is None:
-        xq = torch.empty_strided((M, K), (K, 1), dtype=torch.int8, device=dev)
-    else:
-        _out(xq, (M, K), torch.int8, dev, "xq")
-    if sx is None:
-        sx = torch.empty_strided((M,), (1,), dtype=torch.float32, device=dev)
-    else:
-        _out(sx, (M,), torch.float32, dev, "sx")
-    if xsum is not None:
-        _out(xsum, (M, K // 64), torch.int32, dev, "xsum")
-    elif with_xsum:
-        xsum = torch.empty_strided((M, K // 64), (max(1, K // 64), 1), dtype=torch.int32, device=dev)
-    _same_device(x, weight, residual, h, xq, sx, xsum)
-    _check(lib.qk_rmsnorm_quantize(x.data_ptr(), _ptr(residual), M, K, _ptr(weight), eps, _ptr(h),
-                                   xq.data_ptr(), sx.data_ptr(), _ptr(xsum), _stream(stream)),
-           "qk_rmsnorm_quantize")
-    return h, xq, sx, xsum
+    return _block_calls.rmsnorm_quantize(x, weight, residual, eps, h, xq, sx, xsum, with_xsum,
+                                         _handle(stream))
 
 
 def qk_rope_frequencies(rot, base=10000.0, scaling=QK_ROPE_PLAIN, factor=1.0, trained=0.0, slow=1.0,
@@ -532,7 +474,8 @@ def qk_rope_frequencies(rot, base=10000.0, scaling=QK_ROPE_PLAIN, factor=1.0, tr
         _need(freq, torch.float64, 1, "freq")
         if freq.shape[0] != rot // 2:
             raise ValueError(f"freq must have shape [{rot // 2}]")
-    _same_device(freq)
+        if freq.get_device() != torch.cuda.current_device():
+            raise ValueError(f"freq is on {freq.device}, and the current device is another")
     _check(lib.qk_rope_frequencies(int(rot), float(base), int(scaling), float(factor),
                                    float(trained), float(slow), float(fast), _ptr(freq),
                                    _stream(stream)), "qk_rope_frequencies")
@@ -544,37 +487,7 @@ def qk_rope(q, k, positions, freq, layout=QK_ROPE_HALF, amplitude=1.0, q_out=Non
     """Rotary positions on q bf16 [T, H, D] and k bf16 [T, Hkv, D] (or None), positions int32 [T],
     the first 2 len(freq) dims of each head; returns (q_out, k_out).  Rows may be strided; q_out=q
     (k_out=k) turns them in place."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a [T, H, D] tensor")
-    T, H, D = q.shape
-    qs = _rows(q, H, D, "q")
-    _need(positions, torch.int32, 1, "positions")
-    _need(freq, torch.float64, 1, "freq")
-    if positions.shape[0] != T:
-        raise ValueError(f"positions must have shape [{T}]")
-    if q_out is None:
-        q_out, qos = _new_rows(q, T, H, D), H * D
-    else:
-        qos = _rows(q_out, H, D, "q_out")
-    Hkv = ks = kos = 0
-    if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != 3:
-            raise ValueError("k must be a [T, Hkv, D] tensor")
-        Hkv = k.shape[1]
-        ks = _rows(k, Hkv, D, "k")
-        if k_out is None:
-            k_out, kos = _new_rows(k, k.shape[0], Hkv, D), Hkv * D
-        else:
-            kos = _rows(k_out, Hkv, D, "k_out")
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    if q_out.shape[0] != T or (k is not None and (k.shape[0] != T or k_out.shape[0] != T)):
-        raise ValueError("q, k and the outputs must have the same number of rows")
-    _same_device(q, k, positions, freq, q_out, k_out)
-    _check(lib.qk_rope(q.data_ptr(), qs, q_out.data_ptr(), qos, H, _ptr(k), ks, _ptr(k_out), kos, Hkv,
-                       T, D, 2 * freq.shape[0], int(layout), positions.data_ptr(), freq.data_ptr(),
-                       amplitude, _stream(stream)), "qk_rope")
-    return q_out, k_out
+    return _block_calls.rope(q, k, positions, freq, layout, amplitude, q_out, k_out, _handle(stream))
 
 
 def qk_kv4_cache_size(num_pages: int, Hkv: int, page: int, D: int) -> int:
@@ -582,72 +495,20 @@ def qk_kv4_cache_size(num_pages: int, Hkv: int, page: int, D: int) -> int:
 
 
 def qk_kv4_attention_workspace_size(D: int) -> int:
-    size = _kv4_workspace.get(D)
-    if size is None:
-        size = _kv4_workspace[D] = int(lib.qk_kv4_attention_workspace_size(int(D)))
-    return size
-
-
-_kv4_workspace = {}  # bytes by head dim
-
-
-def _kv4(cache, page_table, kv_lens, cu_rows, T):
-    """(Hkv, D, B, max_pages, num_pages, page) of a cache uint8 [num_pages, Hkv, page, D + D/8]
-    and its requests."""
-    _need(cache, torch.uint8, 4, "cache")
-    _need(page_table, torch.int32, 2, "page_table")
-    _need(kv_lens, torch.int32, 1, "kv_lens")
-    num_pages, Hkv, page, width = cache.shape
-    if width % 9 != 0:
-        raise ValueError("cache must have shape [num_pages, Hkv, page, D + D / 8]")
-    B, max_pages = page_table.shape
-    if kv_lens.shape[0] != B:
-        raise ValueError(f"kv_lens must have shape [{B}]")
-    if cu_rows is not None:
-        _need(cu_rows, torch.int32, 1, "cu_rows")
-        if cu_rows.shape[0] != B + 1:
-            raise ValueError(f"cu_rows must have shape [{B + 1}]")
-    elif B == 0 or T % B != 0:
-        raise ValueError("without cu_rows every request has the same number of rows")
-    return Hkv, width // 9 * 8, B, max_pages, num_pages, page
+    return int(lib.qk_kv4_attention_workspace_size(int(D)))
 
 
 def qk_kv4_append(k, v, cache, page_table, kv_lens, cu_rows=None, stream=None):
     """Writes k, v bf16 [T, Hkv, D] into the 4-bit cache uint8 [num_pages, Hkv, page, D + D/8] as
     the last tokens of their requests: page_table int32 [B, max_pages], kv_lens int32 [B] (new
     tokens included), cu_rows int32 [B + 1] (rows of each request; None: T / B each)."""
-    T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
-    Hkv, D, B, max_pages, num_pages, page = _kv4(cache, page_table, kv_lens, cu_rows, T)
-    ks, vs = _rows(k, Hkv, D, "k"), _rows(v, Hkv, D, "v")
-    if v.shape[0] != T:
-        raise ValueError("k and v must have the same number of rows")
-    _same_device(k, v, cache, page_table, kv_lens, cu_rows)
-    _check(lib.qk_kv4_append(_ptr(k), ks, _ptr(v), vs, T, Hkv, D, _ptr(page_table), B, max_pages,
-                             _ptr(kv_lens), _ptr(cu_rows), _ptr(cache), num_pages, page,
-                             _stream(stream)), "qk_kv4_append")
+    _block_calls.kv4_append(k, v, cache, page_table, kv_lens, cu_rows, _handle(stream))
 
 
 def qk_kv4_gather(cache, page_table, kv_lens, cu_rows, T, k=None, v=None, stream=None):
     """(k, v) bf16 [T, Hkv, D]: the values of the last tokens of each request (cu_rows as in
     qk_kv4_append; all of them where a request's rows number its length)."""
-    T = int(T)
-    Hkv, D, B, max_pages, num_pages, page = _kv4(cache, page_table, kv_lens, cu_rows, T)
-    ks = vs = Hkv * D
-    if k is None:
-        k = _new_rows(cache, T, Hkv, D)
-    else:
-        ks = _rows(k, Hkv, D, "k")
-    if v is None:
-        v = _new_rows(cache, T, Hkv, D)
-    else:
-        vs = _rows(v, Hkv, D, "v")
-    if k.shape[0] != T or v.shape[0] != T:
-        raise ValueError(f"k and v must have {T} rows")
-    _same_device(k, v, cache, page_table, kv_lens, cu_rows)
-    _check(lib.qk_kv4_gather(_ptr(cache), num_pages, page, Hkv, D, _ptr(page_table), B, max_pages,
-                             _ptr(kv_lens), _ptr(cu_rows), T, _ptr(k), ks, _ptr(v), vs,
-                             _stream(stream)), "qk_kv4_gather")
-    return k, v
+    return _block_calls.kv4_gather(cache, page_table, kv_lens, cu_rows, T, k, v, _handle(stream))
 
 
 def qk_kv4_attention(q, cache, page_table, kv_lens, cu_rows=None, scale=None, window=0, sinks=0,
@@ -656,25 +517,5 @@ def qk_kv4_attention(q, cache, page_table, kv_lens, cu_rows=None, scale=None, wi
     over the 4-bit cache; returns bf16 [T, H, D].  window > 0: only the last `window` keys and the
     first `sinks` ones.  Without a workspace, one is taken from torch's allocator (on the current
     stream) or, for another stream, allocated in its order."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a [T, H, D] tensor")
-    T, H = q.shape[0], q.shape[1]
-    Hkv, D, B, max_pages, num_pages, page = _kv4(cache, page_table, kv_lens, cu_rows, T)
-    qs = _rows(q, H, D, "q")
-    out = _new_rows(q, T, H, D) if out is None else _out(out, (T, H, D), torch.bfloat16, q.device, "out")
-    s = _stream(stream)
-    if workspace is not None:
-        ws_bytes = workspace.numel() * workspace.element_size()
-    else:
-        ws_bytes = 0
-        if stream is None or s == _stream(None):
-            ws_bytes = qk_kv4_attention_workspace_size(D)
-            workspace = torch.empty_strided((ws_bytes,), (1,), dtype=torch.uint8, device=q.device)
-    if scale is None:
-        scale = D ** -0.5
-    _same_device(q, out, workspace, cache, page_table, kv_lens, cu_rows)
-    _check(lib.qk_kv4_attention(q.data_ptr(), qs, T, H, Hkv, D, cache.data_ptr(), num_pages, page,
-                                page_table.data_ptr(), B, max_pages, kv_lens.data_ptr(), _ptr(cu_rows),
-                                scale, int(window), int(sinks), _ptr(out), _ptr(workspace),
-                                ws_bytes, s), "qk_kv4_attention")
-    return out
+    return _block_calls.kv4_attention(q, cache, page_table, kv_lens, cu_rows, scale, window, sinks, out,
+                                      workspace, _handle(stream))

@@ -1,4 +1,5 @@
-"""Build libqk.so (the CUDA library behind include/qk.h) in-tree with nvcc.
+"""Build libqk.so (the CUDA library behind include/qk.h) in-tree with nvcc, and
+_block_calls.so (csrc/block_calls.cpp, calls of it for binding.py) with g++.
 
 Every .cu under csrc/ is compiled for sm_100a only
 (``-gencode arch=compute_100a,code=sm_100a``), objects go to ``_build/``, and
@@ -10,10 +11,12 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqk.so")
+CALLS = os.path.join(PKG, "_block_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -69,7 +73,31 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.run([nvcc(), "-shared", *ARCH, "-o", tmp, *objs], check=True)
         os.replace(tmp, LIB)
+    _build_calls(verbose)
     return LIB
+
+
+def _build_calls(verbose: bool) -> None:
+    src = os.path.join(CSRC, "block_calls.cpp")
+    if not _newer(CALLS, [src, os.path.join(INCLUDE, "qk.h")]):
+        return
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc = os.path.join(torch_dir, "include")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = CALLS + f".tmp{os.getpid()}"
+    # (torch's libraries are in the process by the time this one is loaded)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), src, "-o", tmp, "-L", PKG, "-l:libqk.so",
+           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
+           "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed building _block_calls.so")
+    os.replace(tmp, CALLS)
 
 
 if __name__ == "__main__":
