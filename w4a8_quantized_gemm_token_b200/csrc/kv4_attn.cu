@@ -47,6 +47,7 @@
 
 #include <cstdint>
 
+#include "fast_div.cuh"
 #include "kv4.cuh"
 #include "sm100.cuh"
 
@@ -77,22 +78,6 @@ struct Cfg {
   static_assert(SM_HEAD % 16 == 0 && SM_BAR % 16 == 0 && SM_SPAN % 16 == 0, "alignment");
   static_assert(SMEM + 24 * (THREADS + 64) <= 232448, "with the static shared memory");
 };
-
-// n / d for n < 2^31 by a multiplication: 2^p / d rounded up, p = 31 + ceil(log2 d), is
-// off by less than 2^(p - 31) / n in the quotient.
-struct FastDiv {
-  uint32_t m, p;
-  int d;
-};
-FastDiv fast_div(int d) {
-  uint32_t l = 0;
-  while ((1ull << l) < (uint64_t)d) ++l;
-  const uint64_t two_p = 1ull << (31 + l);
-  return FastDiv{(uint32_t)((two_p + (uint64_t)d - 1) / (uint64_t)d), 31 + l, d};
-}
-__device__ __forceinline__ int quot(int n, const FastDiv& f) {
-  return (int)(((uint64_t)(uint32_t)n * f.m) >> f.p);
-}
 
 struct Args {
   const uint16_t* q;

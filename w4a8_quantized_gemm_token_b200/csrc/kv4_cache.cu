@@ -3,7 +3,7 @@
 //
 // Per token, kv head and group of 64 dims, the affine rule of the W4 weights:
 //     s = fp16((max - min) / 15), o = fp16(min),
-//     code = clamp(rne((w - o) fl32(1 / s)), 0, 15)   (0 where s = 0),
+//     code = rne(clamp((w - o) fl32(1 / s), 0, 15))   (0 where s = 0),
 // fp32 arithmetic, one rounding per operation; the value is code s + o.
 //
 // Bound: HBM (4 D bytes of bf16 and 9 D / 8 of record per token and head).  Eight
@@ -66,81 +66,137 @@ __device__ __forceinline__ bool find_token(const Kv4Req& r, const Kv4Cache& c, i
   return true;
 }
 
+// A block takes kThreads / 32 rows, a warp each, and blockIdx.y picks kHeads steps of
+// 32 / LANES heads.  The loads of all of them are in flight at once, and what is
+// computed per group (extremes, scale, reciprocal) is computed for the four steps
+// together, a lane to a step.  9000 rows of 8 heads of 128 dims: heads in turn 21 us,
+// loads together, 210 instructions a head and warp 22 us, as it stands TIME us.
+constexpr int kHeads = 4;
+
+template <int D>
+struct Lane {
+  using L = Kv4<D>;
+  static constexpr int LANES = D / 4;         // of one token and head: K row, then V row
+  static constexpr int STEP = 32 / LANES;     // heads at a time
+  int sub, d8, grp, w8;                       // head of the step; chunk of 8 dims, its group, place
+  bool is_v;
+  __device__ __forceinline__ Lane() {
+    const int lane = threadIdx.x & 31, e = lane % LANES;
+    sub = lane / LANES;
+    is_v = e >= LANES / 2;
+    d8 = e % (LANES / 2);
+    grp = d8 >> 3;
+    w8 = d8 & 7;
+  }
+  // byte offsets in a record, for the token at `place`
+  __device__ __forceinline__ int code(int place) const {
+    return is_v ? L::V_OFF + (((place >> 1) * 8 + w8) * L::NG + grp) * 8 + (place & 1) * 2
+                : place * (D / 2) + (((w8 >> 1) * L::NG + grp) * 2 + (w8 & 1)) * 4;
+  }
+  __device__ __forceinline__ int scale(int place) const {
+    return (is_v ? L::VS_OFF : L::KS_OFF) + (place * L::NG + grp) * 4;
+  }
+};
+
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads)
     kv4_append_kernel(const uint16_t* __restrict__ k, long long k_stride,
                       const uint16_t* __restrict__ v, long long v_stride, const Kv4Req req,
-                      const Kv4Cache cache, int rows_per_block, int* err) {
+                      const Kv4Cache cache, int* err) {
   pdl_launch_dependents();
   pdl_wait();
   using L = Kv4<D>;
-  constexpr int LANES = D / 4;           // of one token and head: K row, then V row
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = lane / LANES, e = lane % LANES;  // D = 64: two heads at a time
-  const bool is_v = e >= LANES / 2;
-  const int d8 = e % (LANES / 2);        // chunk of 8 dims
-  const int grp = d8 >> 3, w8 = d8 & 7;
-  const int tiles = cache.page >> 4;
-  for (int i = warp; i < rows_per_block; i += kThreads / 32) {
-    const int row = blockIdx.x * rows_per_block + i;
-    if (row >= req.T) break;
-    long long at;
-    int place;
-    if (!find_token(req, cache, row, L::REC, &at, &place, err)) continue;  // warp-uniform
-    const uint16_t* src = is_v ? v + row * v_stride : k + row * k_stride;
-    for (int h0 = 0; h0 < cache.Hkv; h0 += 32 / LANES) {
-      const int head = h0 + sub;
-      const bool live = head < cache.Hkv;
-      const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(src + (long long)head * D) + d8)
-                           : make_uint4(0, 0, 0, 0);
-      const uint32_t p[4] = {x.x, x.y, x.z, x.w};
-      float w[8];
+  static_assert(kHeads == 4, "the exchange below");
+  const Lane<D> me;
+  const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (row >= req.T) return;
+  const uint16_t* src = me.is_v ? v + row * v_stride : k + row * k_stride;
+  const int from = blockIdx.y * kHeads * me.STEP, stride = gridDim.y * kHeads * me.STEP;
+  uint4 x[kHeads];
+  auto load = [&](int h0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[2 * j] = __uint_as_float(p[j] << 16);
-        w[2 * j + 1] = __uint_as_float(p[j] & 0xFFFF0000u);
-      }
-      float lo = w[0], hi = w[0];
+    for (int i = 0; i < kHeads; ++i) {
+      const int head = h0 + i * me.STEP + me.sub;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (head < cache.Hkv) x[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)head * D) + me.d8);
+    }
+  };
+  load(from);  // (every row < T is there, whosever it is)
+  long long at;
+  int place;
+  if (!find_token(req, cache, row, L::REC, &at, &place, err)) return;  // warp-uniform
+  const int code = me.code(place), scale = me.scale(place);
+  const long long head_bytes = (long long)(cache.page >> 4) * L::REC;
+  // of the eight lanes of a group, two hold step `mine`'s extremes after the exchange
+  const int lane = threadIdx.x & 31, mine = (lane & 1) * 2 + ((lane >> 1) & 1);
+  for (int h0 = from; h0 < cache.Hkv; h0 += stride) {
+    if (h0 != from) load(h0);
+    uint8_t* rec = cache.base + at + (h0 + me.sub) * head_bytes;
+    uint32_t m[kHeads];  // (max, -min) of the step's group: over the lane, then over the group
 #pragma unroll
-      for (int j = 1; j < 8; ++j) {
-        lo = fminf(lo, w[j]);
-        hi = fmaxf(hi, w[j]);
-      }
+    for (int i = 0; i < kHeads; ++i) {
+      const uint32_t hi = max2(max2(x[i].x, x[i].y), max2(x[i].z, x[i].w));
+      const uint32_t lo = min2(min2(x[i].x, x[i].y), min2(x[i].z, x[i].w)) ^ 0x80008000u;
+      m[i] = max2(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
+    }
+    const bool odd = lane & 1, second = lane & 2;
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
-      }
-      const __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
-      const __half oh = __float2half_rn(lo);
-      const float s = __half2float(sh), off = __half2float(oh);
+    for (int i = 0; i < 2; ++i)
+      m[i] = max2(odd ? m[i + 2] : m[i], __shfl_xor_sync(0xFFFFFFFFu, odd ? m[i] : m[i + 2], 1));
+    uint32_t e = max2(second ? m[1] : m[0], __shfl_xor_sync(0xFFFFFFFFu, second ? m[0] : m[1], 2));
+    e = max2(e, __shfl_xor_sync(0xFFFFFFFFu, e, 4));
+    const float top = __uint_as_float(e << 16), low = -__uint_as_float(e & 0xFFFF0000u);
+    const __half2 so = __halves2half2(__float2half_rn(__fdiv_rn(__fsub_rn(top, low), 15.0f)),
+                                      __float2half_rn(low));
+    // (a scale of 0 has only codes 0)
+    const float inv = __low2float(so) != 0.0f ? __frcp_rn(__low2float(so)) : 0.0f;
+    if (!(lane & 4) && h0 + mine * me.STEP + me.sub < cache.Hkv)
+      *reinterpret_cast<__half2*>(rec + mine * me.STEP * head_bytes + scale) = so;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const int from_lane = (lane & 24) + (i >> 1) + (i & 1) * 2;  // step i's
+      const float off = __half2float(__ushort_as_half(
+          (unsigned short)__shfl_sync(0xFFFFFFFFu, (int)__half_as_ushort(__high2half(so)), from_lane)));
+      const float r = __shfl_sync(0xFFFFFFFFu, inv, from_lane);
+      const uint32_t p[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      // 1.5 2^23 added to a number in [0, 15] rounds it to the nearest even whole one, in the
+      // low bits: eight of them shifted and added leave the codes, and the constants' sum
+      constexpr float kBias = 12582912.0f;
+      constexpr uint32_t kBits = 0x4B400000u;
       uint32_t packed = 0;
-      if (s != 0.0f) {
-        const float r = __fdiv_rn(1.0f, s);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          int q = __float2int_rn(__fmul_rn(__fsub_rn(w[j], off), r));
-          q = max(0, min(15, q));
-          packed |= (uint32_t)q << (4 * j);
-        }
+      for (int j = 7; j >= 0; --j) {
+        const float w = __uint_as_float((j & 1) ? p[j >> 1] & 0xFFFF0000u : p[j >> 1] << 16);
+        const float y = fminf(fmaxf(__fmul_rn(__fsub_rn(w, off), r), 0.0f), 15.0f);
+        packed = (packed << 4) + __float_as_uint(__fadd_rn(y, kBias));
       }
-      if (!live) continue;
-      uint8_t* rec = cache.base + at + (long long)head * tiles * L::REC;
-      if (!is_v) {
-        reinterpret_cast<uint32_t*>(rec + place * (D / 2))[((w8 >> 1) * L::NG + grp) * 2 + (w8 & 1)] =
-            packed;
+      packed -= kBits * 0x11111111u;
+      if (h0 + i * me.STEP + me.sub >= cache.Hkv) continue;
+      uint8_t* dst = rec + i * me.STEP * head_bytes + code;
+      if (!me.is_v) {
+        *reinterpret_cast<uint32_t*>(dst) = packed;
       } else {
-        uint16_t* dst = reinterpret_cast<uint16_t*>(
-            rec + L::V_OFF + (((place >> 1) * 8 + w8) * L::NG + grp) * 8 + (place & 1) * 2);
-        dst[0] = (uint16_t)packed;
-        dst[2] = (uint16_t)(packed >> 16);
-      }
-      if (w8 == 0) {
-        __half2* sc = reinterpret_cast<__half2*>(rec + (is_v ? L::VS_OFF : L::KS_OFF));
-        sc[place * L::NG + grp] = __halves2half2(sh, oh);
+        reinterpret_cast<uint16_t*>(dst)[0] = (uint16_t)packed;
+        reinterpret_cast<uint16_t*>(dst)[2] = (uint16_t)(packed >> 16);
       }
     }
   }
+}
+
+// A small whole number as fp32: in the low bits of 2^23, which is taken off again.
+__device__ __forceinline__ float whole(uint32_t c) {
+  return __uint_as_float(c | 0x4B000000u) - 8388608.0f;
 }
 
 // Rows whose token is nowhere (a length or page id out of bounds) come back as
@@ -148,65 +204,67 @@ __global__ void __launch_bounds__(kThreads)
 template <int D>
 __global__ void __launch_bounds__(kThreads)
     kv4_gather_kernel(const Kv4Req req, const Kv4Cache cache, uint16_t* __restrict__ k,
-                      long long k_stride, uint16_t* __restrict__ v, long long v_stride,
-                      int rows_per_block, int* err) {
+                      long long k_stride, uint16_t* __restrict__ v, long long v_stride, int* err) {
   pdl_launch_dependents();
   pdl_wait();
   using L = Kv4<D>;
-  constexpr int LANES = D / 4;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = lane / LANES, e = lane % LANES;
-  const bool is_v = e >= LANES / 2;
-  const int d8 = e % (LANES / 2);
-  const int grp = d8 >> 3, w8 = d8 & 7;
+  const Lane<D> me;
+  const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (row >= req.T) return;
   const int tiles = cache.page >> 4;
-  for (int i = warp; i < rows_per_block; i += kThreads / 32) {
-    const int row = blockIdx.x * rows_per_block + i;
-    if (row >= req.T) break;
-    long long at = 0;
-    int place = 0;
-    const bool found = find_token(req, cache, row, L::REC, &at, &place, err);
-    if (!found) {
-      const int b = find_request(req, row);
-      if (b >= req.B || row < kv4_seq(req, b, err).row0) continue;
-    }
-    uint16_t* dst = is_v ? v + row * v_stride : k + row * k_stride;
-    for (int head = sub; head < cache.Hkv; head += 32 / LANES) {
-      uint32_t out[4] = {0, 0, 0, 0};
-      if (found) {
-        const uint8_t* rec = cache.base + at + (long long)head * tiles * L::REC;
-        uint32_t packed;
-        if (!is_v) {
-          packed = reinterpret_cast<const uint32_t*>(
-              rec + place * (D / 2))[((w8 >> 1) * L::NG + grp) * 2 + (w8 & 1)];
-        } else {
-          const uint16_t* src = reinterpret_cast<const uint16_t*>(
-              rec + L::V_OFF + (((place >> 1) * 8 + w8) * L::NG + grp) * 8 + (place & 1) * 2);
-          packed = src[0] | (uint32_t)src[2] << 16;
-        }
-        const __half2 so = reinterpret_cast<const __half2*>(
-            rec + (is_v ? L::VS_OFF : L::KS_OFF))[place * L::NG + grp];
-        const float s = __low2float(so), o = __high2float(so);
+  long long at = 0;
+  int place = 0;
+  const bool found = find_token(req, cache, row, L::REC, &at, &place, err);
+  if (!found) {
+    const int b = find_request(req, row);
+    if (b >= req.B || row < kv4_seq(req, b, err).row0) return;
+  }
+  uint16_t* dst = me.is_v ? v + row * v_stride : k + row * k_stride;
+  const int code = me.code(place), scale = me.scale(place);
+  const int stride = gridDim.y * kHeads * me.STEP;
+  for (int h0 = blockIdx.y * kHeads * me.STEP; h0 < cache.Hkv; h0 += stride) {
+    uint32_t packed[kHeads];
+    __half2 so[kHeads];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // code * scale is exact in fp32 (4 + 11 bits): one rounding of the sum, then bf16's
-          const float a = fmaf((float)((packed >> (8 * j)) & 15u), s, o);
-          const float b = fmaf((float)((packed >> (8 * j + 4)) & 15u), s, o);
-          const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-          out[j] = *reinterpret_cast<const uint32_t*>(&r);
-        }
+    for (int i = 0; i < kHeads; ++i) {
+      const int head = h0 + i * me.STEP + me.sub;
+      packed[i] = 0;
+      so[i] = __half2half2(__ushort_as_half(0));
+      if (!found || head >= cache.Hkv) continue;
+      const uint8_t* rec = cache.base + at + (long long)head * tiles * L::REC;
+      if (!me.is_v) {
+        packed[i] = *reinterpret_cast<const uint32_t*>(rec + code);
+      } else {
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(rec + code);
+        packed[i] = src[0] | (uint32_t)src[2] << 16;
       }
-      *(reinterpret_cast<uint4*>(dst + (long long)head * D) + d8) =
+      so[i] = *reinterpret_cast<const __half2*>(rec + scale);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const int head = h0 + i * me.STEP + me.sub;
+      if (head >= cache.Hkv) continue;
+      const float s = __low2float(so[i]), o = __high2float(so[i]);
+      uint32_t out[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // code * scale is exact in fp32 (4 + 11 bits): one rounding of the sum, then bf16's
+        const float a = fmaf(whole((packed[i] >> (8 * j)) & 15u), s, o);
+        const float b = fmaf(whole((packed[i] >> (8 * j + 4)) & 15u), s, o);
+        const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+        out[j] = *reinterpret_cast<const uint32_t*>(&r);
+      }
+      *(reinterpret_cast<uint4*>(dst + (long long)head * D) + me.d8) =
           make_uint4(out[0], out[1], out[2], out[3]);
     }
   }
 }
 
-void grid_of(int64_t T, int* rows, cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr,
+void grid_of(int64_t T, int Hkv, int D, cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr,
              cudaStream_t s) {
-  // a warp per row; more rows per block once every SM has its share of blocks
-  *rows = kThreads / 32;
-  cfg->gridDim = dim3((unsigned)((T + *rows - 1) / *rows));
+  const int rows = kThreads / 32, heads = kHeads * (D == 64 ? 2 : 1);
+  const int groups = (Hkv + heads - 1) / heads;
+  cfg->gridDim = dim3((unsigned)((T + rows - 1) / rows), (unsigned)(groups < 64 ? groups : 64));
   cfg->blockDim = dim3(kThreads);
   cfg->stream = s;
   attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -222,11 +280,10 @@ cudaError_t launch_kv4_append(const uint16_t* k, int64_t k_stride, const uint16_
                               cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  int rows;
-  grid_of(req.T, &rows, &cfg, attr, s);
+  grid_of(req.T, cache.Hkv, cache.D, &cfg, attr, s);
   auto kernel = cache.D == 64 ? kv4_append_kernel<64> : kv4_append_kernel<128>;
   return cudaLaunchKernelEx(&cfg, kernel, k, (long long)k_stride, v, (long long)v_stride, req,
-                            cache, rows, err);
+                            cache, err);
 }
 
 cudaError_t launch_kv4_gather(const Kv4Req& req, const Kv4Cache& cache, uint16_t* k,
@@ -234,11 +291,10 @@ cudaError_t launch_kv4_gather(const Kv4Req& req, const Kv4Cache& cache, uint16_t
                               cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  int rows;
-  grid_of(req.T, &rows, &cfg, attr, s);
+  grid_of(req.T, cache.Hkv, cache.D, &cfg, attr, s);
   auto kernel = cache.D == 64 ? kv4_gather_kernel<64> : kv4_gather_kernel<128>;
   return cudaLaunchKernelEx(&cfg, kernel, req, cache, k, (long long)k_stride, v,
-                            (long long)v_stride, rows, err);
+                            (long long)v_stride, err);
 }
 
 }  // namespace qk

@@ -16,6 +16,7 @@
 
 #include <cstdint>
 
+#include "fast_div.cuh"
 #include "qk_internal.h"
 #include "sm100.cuh"
 
@@ -37,14 +38,18 @@ struct RopeArgs {
   uint16_t* out[2];
   long long in_stride[2], out_stride[2];  // elements between tokens
   int heads[2];
-  int T, D, rot, tokens;  // tokens per block
+  int T, D, rot, tokens;       // tokens per block
+  FastDiv per_token, per_head;  // steps
   const int32_t* positions;
   const double* freq;
   float amplitude;
 };
 
-// kVec: 16-byte chunks (half layout: rot % 16 == 0, interleaved: rot % 8 == 0);
-// otherwise one pair or one copied element per step.
+// kVec: 16-byte chunks (half layout: rot % 16 == 0, interleaved: rot % 8 == 0), with
+// kUnroll steps' loads of a thread in flight, the first ones before the angles are
+// made; otherwise one pair or one copied element per step.
+constexpr int unroll(bool half) { return half ? 2 : 4; }  // (a step of the half layout loads two chunks)
+
 template <bool kHalf, bool kVec>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs p) {
   pdl_launch_dependents();
@@ -53,68 +58,106 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs p) {
   const int half = p.rot >> 1;
   const int t0 = blockIdx.x * p.tokens;
   const int nt = min(p.tokens, p.T - t0);
-  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const int tok = i / half, f = i - tok * half;
-    const double turns = (double)__ldg(p.positions + t0 + tok) * __ldg(p.freq + f);
-    const float frac = (float)(turns - rint(turns));  // [-1/2, 1/2]
-    float s, c;
-    sincospif(2.0f * frac, &s, &c);
-    cs[i] = c * p.amplitude;
-    sn[i] = s * p.amplitude;
-  }
-  __syncthreads();
+  auto angles = [&]() {
+    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+      const int tok = i / half, f = i - tok * half;
+      const double turns = (double)__ldg(p.positions + t0 + tok) * __ldg(p.freq + f);
+      const float frac = (float)(turns - rint(turns));  // [-1/2, 1/2]
+      float s, c;
+      sincospif(2.0f * frac, &s, &c);
+      cs[i] = c * p.amplitude;
+      sn[i] = s * p.amplitude;
+    }
+    __syncthreads();
+  };
   const int rotated = kVec ? (kHalf ? p.rot >> 4 : p.rot >> 3) : half;
-  const int copied = kVec ? (p.D - p.rot) >> 3 : p.D - p.rot;
-  const int per_head = rotated + copied;
-  const int heads = p.heads[0] + p.heads[1];
-  const int per_token = heads * per_head;
-  for (int i = threadIdx.x; i < nt * per_token; i += kThreads) {
-    const int tok = i / per_token, rest = i - tok * per_token;
-    int hd = rest / per_head;
-    const int e = rest - hd * per_head;
+  const int steps = nt * p.per_token.d;
+  struct Step {
+    const uint16_t* src;
+    uint16_t* dst;
+    int e, angle;  // chunk of the head; the token's first angle
+  };
+  auto step = [&](int i) {
+    Step r;
+    const int tok = quot(i, p.per_token), rest = i - tok * p.per_token.d;
+    int hd = quot(rest, p.per_head);
+    r.e = rest - hd * p.per_head.d;
     const int which = hd >= p.heads[0];
     if (which) hd -= p.heads[0];
-    const uint16_t* src = p.in[which] + (t0 + tok) * p.in_stride[which] + (long long)hd * p.D;
-    uint16_t* dst = p.out[which] + (t0 + tok) * p.out_stride[which] + (long long)hd * p.D;
-    const float* c = cs + tok * half;
-    const float* s = sn + tok * half;
-    if (e >= rotated) {  // behind the rotated part
-      if (src == dst) continue;
-      if constexpr (kVec)
-        *reinterpret_cast<uint4*>(dst + p.rot + 8 * (e - rotated)) =
-            *reinterpret_cast<const uint4*>(src + p.rot + 8 * (e - rotated));
-      else
-        dst[p.rot + e - rotated] = src[p.rot + e - rotated];
-    } else if constexpr (kVec && kHalf) {
-      const uint4 a4 = *reinterpret_cast<const uint4*>(src + 8 * e);
-      const uint4 b4 = *reinterpret_cast<const uint4*>(src + half + 8 * e);
-      const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
-      uint32_t u[4], v[4];
+    r.src = p.in[which] + (t0 + tok) * p.in_stride[which] + (long long)hd * p.D;
+    r.dst = p.out[which] + (t0 + tok) * p.out_stride[which] + (long long)hd * p.D;
+    r.angle = tok * half;
+    return r;
+  };
+  if constexpr (kVec) {
+    constexpr int U = unroll(kHalf);
+    for (int base = 0; base < steps; base += U * kThreads) {
+      Step st[U];
+      uint4 a4[U], b4[U];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float c0 = c[8 * e + 2 * j], c1 = c[8 * e + 2 * j + 1];
-        const float s0 = s[8 * e + 2 * j], s1 = s[8 * e + 2 * j + 1];
-        u[j] = pack16(lo16(a[j]) * c0 - lo16(b[j]) * s0, hi16(a[j]) * c1 - hi16(b[j]) * s1);
-        v[j] = pack16(lo16(b[j]) * c0 + lo16(a[j]) * s0, hi16(b[j]) * c1 + hi16(a[j]) * s1);
+      for (int u = 0; u < U; ++u) {
+        const int i = base + u * kThreads + threadIdx.x;
+        if (i >= steps) continue;
+        st[u] = step(i);
+        const bool turned = st[u].e < rotated;
+        const int at = kHalf && !turned ? p.rot + 8 * (st[u].e - rotated) : 8 * st[u].e;
+        st[u].src += at;
+        st[u].dst += at;
+        a4[u] = __ldcs(reinterpret_cast<const uint4*>(st[u].src));
+        if (kHalf && turned) b4[u] = __ldcs(reinterpret_cast<const uint4*>(st[u].src + half));
       }
-      *reinterpret_cast<uint4*>(dst + 8 * e) = make_uint4(u[0], u[1], u[2], u[3]);
-      *reinterpret_cast<uint4*>(dst + half + 8 * e) = make_uint4(v[0], v[1], v[2], v[3]);
-    } else if constexpr (kVec) {
-      const uint4 a4 = *reinterpret_cast<const uint4*>(src + 8 * e);
-      const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w};
-      uint32_t u[4];
+      if (base == 0) angles();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float c0 = c[4 * e + j], s0 = s[4 * e + j];
-        u[j] = pack16(lo16(a[j]) * c0 - hi16(a[j]) * s0, hi16(a[j]) * c0 + lo16(a[j]) * s0);
+      for (int u = 0; u < U; ++u) {
+        if (base + u * kThreads + threadIdx.x >= steps) continue;
+        uint4* dst = reinterpret_cast<uint4*>(st[u].dst);
+        if (st[u].e >= rotated) {  // behind the rotated part
+          if (st[u].src != st[u].dst) *dst = a4[u];
+          continue;
+        }
+        const uint32_t a[4] = {a4[u].x, a4[u].y, a4[u].z, a4[u].w};
+        uint32_t x[4];
+        if constexpr (kHalf) {
+          const float4* c = reinterpret_cast<const float4*>(cs + st[u].angle + 8 * st[u].e);
+          const float4* s = reinterpret_cast<const float4*>(sn + st[u].angle + 8 * st[u].e);
+          const uint32_t b[4] = {b4[u].x, b4[u].y, b4[u].z, b4[u].w};
+          uint32_t y[4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float4 cc = c[j], ss = s[j];
+            const uint32_t a0 = a[2 * j], a1 = a[2 * j + 1], b0 = b[2 * j], b1 = b[2 * j + 1];
+            x[2 * j] = pack16(lo16(a0) * cc.x - lo16(b0) * ss.x, hi16(a0) * cc.y - hi16(b0) * ss.y);
+            x[2 * j + 1] = pack16(lo16(a1) * cc.z - lo16(b1) * ss.z, hi16(a1) * cc.w - hi16(b1) * ss.w);
+            y[2 * j] = pack16(lo16(b0) * cc.x + lo16(a0) * ss.x, hi16(b0) * cc.y + hi16(a0) * ss.y);
+            y[2 * j + 1] = pack16(lo16(b1) * cc.z + lo16(a1) * ss.z, hi16(b1) * cc.w + hi16(a1) * ss.w);
+          }
+          *reinterpret_cast<uint4*>(st[u].dst + half) = make_uint4(y[0], y[1], y[2], y[3]);
+        } else {
+          const float4 cc = *reinterpret_cast<const float4*>(cs + st[u].angle + 4 * st[u].e);
+          const float4 ss = *reinterpret_cast<const float4*>(sn + st[u].angle + 4 * st[u].e);
+          const float c[4] = {cc.x, cc.y, cc.z, cc.w}, s[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            x[j] = pack16(lo16(a[j]) * c[j] - hi16(a[j]) * s[j], hi16(a[j]) * c[j] + lo16(a[j]) * s[j]);
+        }
+        *dst = make_uint4(x[0], x[1], x[2], x[3]);
       }
-      *reinterpret_cast<uint4*>(dst + 8 * e) = make_uint4(u[0], u[1], u[2], u[3]);
-    } else {
-      const int ia = kHalf ? e : 2 * e, ib = kHalf ? e + half : 2 * e + 1;
-      const float a = lo16(src[ia]), b = lo16(src[ib]);
-      const uint32_t r = pack16(a * c[e] - b * s[e], b * c[e] + a * s[e]);
-      dst[ia] = (uint16_t)r;
-      dst[ib] = (uint16_t)(r >> 16);
+    }
+  } else {
+    angles();
+    for (int i = threadIdx.x; i < steps; i += kThreads) {
+      const Step r = step(i);
+      if (r.e >= rotated) {
+        const int at = p.rot + r.e - rotated;
+        if (r.src != r.dst) r.dst[at] = r.src[at];
+        continue;
+      }
+      const int ia = kHalf ? r.e : 2 * r.e, ib = kHalf ? r.e + half : 2 * r.e + 1;
+      const float a = lo16(r.src[ia]), b = lo16(r.src[ib]);
+      const float c = cs[r.angle + r.e], s = sn[r.angle + r.e];
+      const uint32_t y = pack16(a * c - b * s, b * c + a * s);
+      r.dst[ia] = (uint16_t)y;
+      r.dst[ib] = (uint16_t)(y >> 16);
     }
   }
 }
@@ -153,15 +196,17 @@ cudaError_t launch_rope(const uint16_t* q, int64_t q_stride, uint16_t* q_out, in
   a.heads[1] = k != nullptr ? (int)Hkv : 0;
   a.T = (int)T; a.D = (int)D; a.rot = (int)rot;
   a.positions = positions; a.freq = freq; a.amplitude = amplitude;
-  // several tokens per block where one token's heads do not fill it, as long as
-  // their angles fit and every SM keeps a block
-  const int64_t steps = (H + a.heads[1]) * (D / 16);
+  const bool vec = half ? rot % 16 == 0 : rot % 8 == 0;
+  const int per_head = vec ? (int)((half ? rot / 16 : rot / 8) + (D - rot) / 8) : (int)(rot / 2 + D - rot);
+  a.per_head = fast_div(per_head);
+  a.per_token = fast_div(per_head * (a.heads[0] + a.heads[1]));
+  // as many tokens per block as one pass of its threads holds, as long as their angles
+  // fit and every SM keeps a block
   int64_t tokens = 1;
-  while (tokens < 16 && tokens * steps < 2 * kThreads && 2 * tokens * (rot / 2) <= kMaxPairs &&
-         T / (2 * tokens) >= num_sms())
+  while (tokens < 16 && 2 * tokens * a.per_token.d <= unroll(half) * kThreads &&
+         2 * tokens * (rot / 2) <= kMaxPairs && T / (2 * tokens) >= num_sms())
     tokens *= 2;
   a.tokens = (int)tokens;
-  const bool vec = half ? rot % 16 == 0 : rot % 8 == 0;
   void (*kernel)(RopeArgs) = half ? (vec ? rope_kernel<true, true> : rope_kernel<true, false>)
                                   : (vec ? rope_kernel<false, true> : rope_kernel<false, false>);
   cudaLaunchConfig_t cfg = {};
