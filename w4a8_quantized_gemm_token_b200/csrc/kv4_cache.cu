@@ -13,15 +13,17 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
+#include "fast_div.cuh"
 #include "kv4.cuh"
 #include "sm100.cuh"
 
 namespace qk {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // The request that row belongs to, by the whole warp (B when it is behind the
 // last one): the number of bounds cu[1 .. B] that are <= row, narrowed 32-fold a step.
@@ -40,37 +42,55 @@ __device__ __forceinline__ int find_request(const Kv4Req& r, int row) {
   return lo;
 }
 
-// Where row `row` of the call lives: the byte offset of its record (for kv head 0)
-// and its place in it; false (recorded, unless it is behind the last request) if nowhere.
-__device__ __forceinline__ bool find_token(const Kv4Req& r, const Kv4Cache& c, int row, int rec,
-                                           long long* at, int* place, int* err) {
-  const int b = find_request(r, row);
-  if (b >= r.B) return false;
-  const Kv4Seq s = kv4_seq(r, b, err);
-  const int pos = s.len - s.n + (row - s.row0);
-  if (row < s.row0) return false;  // in front of the first request
-  if (pos < 0 || row >= s.row0 + s.n) {  // no such token; or row bounds that fall
-    record_index(err);
-    return false;
+// Where a row of the call lives.
+struct Place {
+  long long at;  // byte offset of its record, for kv head 0
+  int in;        // its token in the record; -1: nowhere (recorded); -2: nobody's row
+};
+
+// Of the warp's rows first .. first + n - 1 (n <= 32), lane r's: the rows of one
+// request find it together, and every row's page is looked up at the same time.
+__device__ __forceinline__ Place find_tokens(const Kv4Req& r, const Kv4Cache& c, const FastDiv& by_page,
+                                             int first, int n, int rec, int* err) {
+  const int lane = threadIdx.x & 31, row = first + lane;
+  Place p = {0, -2};
+  uint32_t todo = 0xFFFFFFFFu >> (32 - n);
+  while (todo) {
+    const int lead = first + __ffs(todo) - 1;
+    const int b = find_request(r, lead);
+    if (b >= r.B) break;  // behind the last request, and so are the rows that follow
+    const Kv4Seq s = kv4_seq(r, b, err);
+    // (row bounds that fall may leave the leading row outside of its request)
+    const bool mine = (todo >> lane & 1u) && (row == lead || (row >= s.row0 && row < s.row0 + s.n));
+    if (mine && row >= s.row0) {
+      const int pos = s.len - s.n + (row - s.row0);
+      p.in = -1;
+      if (pos < 0 || row >= s.row0 + s.n) {  // no such token
+        record_index(err);
+      } else {
+        const int pg = quot(pos, by_page);
+        const int id = __ldg(r.page_table + (long long)b * r.max_pages + pg);
+        if (id < 0 || id >= c.num_pages) {
+          record_index(err);
+        } else {
+          const int off = pos - pg * c.page;
+          p.at = ((long long)id * c.Hkv * (c.page >> 4) + (off >> 4)) * rec;
+          p.in = off & 15;
+        }
+      }
+    }
+    todo &= ~__ballot_sync(0xFFFFFFFFu, mine);
   }
-  const int pg = pos / c.page;
-  const int id = __ldg(r.page_table + (long long)b * r.max_pages + pg);
-  if (id < 0 || id >= c.num_pages) {
-    record_index(err);
-    return false;
-  }
-  const int in = pos - pg * c.page;
-  const int tiles = c.page >> 4;
-  *at = ((long long)id * c.Hkv * tiles + (in >> 4)) * rec;
-  *place = in & 15;
-  return true;
+  return p;
 }
 
-// A block takes kThreads / 32 rows, a warp each, and blockIdx.y picks kHeads steps of
-// 32 / LANES heads.  The loads of all of them are in flight at once, and what is
-// computed per group (extremes, scale, reciprocal) is computed for the four steps
-// together, a lane to a step.  9000 rows of 8 heads of 128 dims: heads in turn 21 us,
-// loads together, 210 instructions a head and warp 22 us, as it stands TIME us.
+// A warp takes a run of rows (as many as leave every SM its warps) and blockIdx.y
+// picks kHeads steps of 32 / LANES heads: the rows' places are looked up together, a
+// lane to a row, the loads of a row's steps are in flight at once and those of the next
+// row while it is worked on, and what is computed per group (extremes, scale,
+// reciprocal) is computed for the four steps together, a lane to a step.  10144 rows of 8
+// heads of 128 dims: a row to a warp and head after head 21 us, four heads at once 17.5
+// us, runs of 5 rows 16 us (read back: 22, 18, 15 us).
 constexpr int kHeads = 4;
 
 template <int D>
@@ -113,36 +133,53 @@ template <int D>
 __global__ void __launch_bounds__(kThreads)
     kv4_append_kernel(const uint16_t* __restrict__ k, long long k_stride,
                       const uint16_t* __restrict__ v, long long v_stride, const Kv4Req req,
-                      const Kv4Cache cache, int* err) {
+                      const Kv4Cache cache, const FastDiv by_page, int run, int* err) {
   pdl_launch_dependents();
   pdl_wait();
   using L = Kv4<D>;
   static_assert(kHeads == 4, "the exchange below");
   const Lane<D> me;
-  const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (row >= req.T) return;
-  const uint16_t* src = me.is_v ? v + row * v_stride : k + row * k_stride;
-  const int from = blockIdx.y * kHeads * me.STEP, stride = gridDim.y * kHeads * me.STEP;
-  uint4 x[kHeads];
-  auto load = [&](int h0) {
+  const int first = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * run;
+  const int n = min(run, req.T - first);
+  if (n <= 0) return;
+  const int groups = gridDim.y * kHeads * me.STEP;
+  uint4 next[kHeads];
+  // step q: row first + q % n, head group q / n
+  auto load = [&](int r, int h0) {
+    const long long row = first + r;
+    const uint16_t* src = me.is_v ? v + row * v_stride : k + row * k_stride;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
       const int head = h0 + i * me.STEP + me.sub;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (head < cache.Hkv) x[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)head * D) + me.d8);
+      next[i] = make_uint4(0, 0, 0, 0);
+      if (head < cache.Hkv) next[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)head * D) + me.d8);
     }
   };
-  load(from);  // (every row < T is there, whosever it is)
-  long long at;
-  int place;
-  if (!find_token(req, cache, row, L::REC, &at, &place, err)) return;  // warp-uniform
-  const int code = me.code(place), scale = me.scale(place);
+  int r = 0, h0 = blockIdx.y * kHeads * me.STEP;
+  load(r, h0);  // (every row < T is there, whosever it is)
+  const Place all = find_tokens(req, cache, by_page, first, n, L::REC, err);
   const long long head_bytes = (long long)(cache.page >> 4) * L::REC;
   // of the eight lanes of a group, two hold step `mine`'s extremes after the exchange
   const int lane = threadIdx.x & 31, mine = (lane & 1) * 2 + ((lane >> 1) & 1);
-  for (int h0 = from; h0 < cache.Hkv; h0 += stride) {
-    if (h0 != from) load(h0);
-    uint8_t* rec = cache.base + at + (h0 + me.sub) * head_bytes;
+  for (;;) {
+    const int row = r, head0 = h0;
+    uint4 x[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) x[i] = next[i];
+    if (++r == n) {
+      r = 0;
+      h0 += groups;
+    }
+    const bool more = h0 < cache.Hkv;
+    if (more) load(r, h0);
+    const long long at = __shfl_sync(0xFFFFFFFFu, all.at, row);
+    const int place = __shfl_sync(0xFFFFFFFFu, all.in, row);
+    if (place < 0) {  // (the whole warp)
+      if (!more) break;
+      continue;
+    }
+    const int code = me.code(place), scale = me.scale(place);
+    uint8_t* rec = cache.base + at + (head0 + me.sub) * head_bytes;
     uint32_t m[kHeads];  // (max, -min) of the step's group: over the lane, then over the group
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
@@ -160,8 +197,8 @@ __global__ void __launch_bounds__(kThreads)
     const __half2 so = __halves2half2(__float2half_rn(__fdiv_rn(__fsub_rn(top, low), 15.0f)),
                                       __float2half_rn(low));
     // (a scale of 0 has only codes 0)
-    const float inv = __low2float(so) != 0.0f ? __frcp_rn(__low2float(so)) : 0.0f;
-    if (!(lane & 4) && h0 + mine * me.STEP + me.sub < cache.Hkv)
+    const float inv = __low2float(so) != 0.0f ? 0.0625f * __frcp_rn(__low2float(so)) : 0.0f;
+    if (!(lane & 4) && head0 + mine * me.STEP + me.sub < cache.Hkv)
       *reinterpret_cast<__half2*>(rec + mine * me.STEP * head_bytes + scale) = so;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
@@ -170,19 +207,20 @@ __global__ void __launch_bounds__(kThreads)
           (unsigned short)__shfl_sync(0xFFFFFFFFu, (int)__half_as_ushort(__high2half(so)), from_lane)));
       const float r = __shfl_sync(0xFFFFFFFFu, inv, from_lane);
       const uint32_t p[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      // 1.5 2^23 added to a number in [0, 15] rounds it to the nearest even whole one, in the
-      // low bits: eight of them shifted and added leave the codes, and the constants' sum
-      constexpr float kBias = 12582912.0f;
-      constexpr uint32_t kBits = 0x4B400000u;
+      // Everything by 1/16, so that the product's saturation is the clamp at 0.  1.5 2^19
+      // added to a number below 1 rounds it to the nearest even 16th, in the low bits: eight
+      // of them shifted and added leave the codes, and the constants' sum
+      constexpr float kBias = 786432.0f;
+      constexpr uint32_t kBits = 0x49400000u;
       uint32_t packed = 0;
 #pragma unroll
       for (int j = 7; j >= 0; --j) {
         const float w = __uint_as_float((j & 1) ? p[j >> 1] & 0xFFFF0000u : p[j >> 1] << 16);
-        const float y = fminf(fmaxf(__fmul_rn(__fsub_rn(w, off), r), 0.0f), 15.0f);
+        const float y = fminf(__saturatef(__fmul_rn(__fsub_rn(w, off), r)), 0.9375f);
         packed = (packed << 4) + __float_as_uint(__fadd_rn(y, kBias));
       }
       packed -= kBits * 0x11111111u;
-      if (h0 + i * me.STEP + me.sub >= cache.Hkv) continue;
+      if (head0 + i * me.STEP + me.sub >= cache.Hkv) continue;
       uint8_t* dst = rec + i * me.STEP * head_bytes + code;
       if (!me.is_v) {
         *reinterpret_cast<uint32_t*>(dst) = packed;
@@ -191,6 +229,7 @@ __global__ void __launch_bounds__(kThreads)
         reinterpret_cast<uint16_t*>(dst)[2] = (uint16_t)(packed >> 16);
       }
     }
+    if (!more) break;
   }
 }
 
@@ -203,68 +242,91 @@ __device__ __forceinline__ float whole(uint32_t c) {
 // zeros; rows behind the last request are left as they were.
 template <int D>
 __global__ void __launch_bounds__(kThreads)
-    kv4_gather_kernel(const Kv4Req req, const Kv4Cache cache, uint16_t* __restrict__ k,
-                      long long k_stride, uint16_t* __restrict__ v, long long v_stride, int* err) {
+    kv4_gather_kernel(const Kv4Req req, const Kv4Cache cache, const FastDiv by_page, int run,
+                      uint16_t* __restrict__ k, long long k_stride, uint16_t* __restrict__ v,
+                      long long v_stride, int* err) {
   pdl_launch_dependents();
   pdl_wait();
   using L = Kv4<D>;
   const Lane<D> me;
-  const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (row >= req.T) return;
-  const int tiles = cache.page >> 4;
-  long long at = 0;
+  const int first = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * run;
+  const int n = min(run, req.T - first);
+  if (n <= 0) return;
+  const long long head_bytes = (long long)(cache.page >> 4) * L::REC;
+  const int groups = gridDim.y * kHeads * me.STEP;
+  const Place all = find_tokens(req, cache, by_page, first, n, L::REC, err);
+  uint2 codes[kHeads];
+  uint32_t so[kHeads];
   int place = 0;
-  const bool found = find_token(req, cache, row, L::REC, &at, &place, err);
-  if (!found) {
-    const int b = find_request(req, row);
-    if (b >= req.B || row < kv4_seq(req, b, err).row0) return;
-  }
-  uint16_t* dst = me.is_v ? v + row * v_stride : k + row * k_stride;
-  const int code = me.code(place), scale = me.scale(place);
-  const int stride = gridDim.y * kHeads * me.STEP;
-  for (int h0 = blockIdx.y * kHeads * me.STEP; h0 < cache.Hkv; h0 += stride) {
+  auto load = [&](int r, int h0) {
+    const long long at = __shfl_sync(0xFFFFFFFFu, all.at, r);
+    place = __shfl_sync(0xFFFFFFFFu, all.in, r);
+    const uint8_t* rec = cache.base + at + (h0 + me.sub) * head_bytes;
+    const int code = me.code(place) & ~3, scale = me.scale(place);  // (a V word holds two tokens)
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      codes[i] = make_uint2(0, 0);
+      so[i] = 0;
+      if (place < 0 || h0 + i * me.STEP + me.sub >= cache.Hkv) continue;
+      const uint8_t* src = rec + i * me.STEP * head_bytes;
+      if (me.is_v)
+        codes[i] = __ldg(reinterpret_cast<const uint2*>(src + code));
+      else
+        codes[i].x = __ldg(reinterpret_cast<const uint32_t*>(src + code));
+      so[i] = __ldg(reinterpret_cast<const uint32_t*>(src + scale));
+    }
+  };
+  int r = 0, h0 = blockIdx.y * kHeads * me.STEP;
+  load(r, h0);
+  for (;;) {
+    const long long row = first + r;
+    const int head0 = h0;
+    const bool owned = place != -2;
+    const uint32_t pick = !me.is_v ? 0x3210u : (place & 1) ? 0x7632u : 0x5410u;
     uint32_t packed[kHeads];
-    __half2 so[kHeads];
+    float s[kHeads], o[kHeads];
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-      const int head = h0 + i * me.STEP + me.sub;
-      packed[i] = 0;
-      so[i] = __half2half2(__ushort_as_half(0));
-      if (!found || head >= cache.Hkv) continue;
-      const uint8_t* rec = cache.base + at + (long long)head * tiles * L::REC;
-      if (!me.is_v) {
-        packed[i] = *reinterpret_cast<const uint32_t*>(rec + code);
-      } else {
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(rec + code);
-        packed[i] = src[0] | (uint32_t)src[2] << 16;
-      }
-      so[i] = *reinterpret_cast<const __half2*>(rec + scale);
+      packed[i] = __byte_perm(codes[i].x, codes[i].y, pick);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&so[i]));
+      s[i] = f.x;
+      o[i] = f.y;
     }
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      const int head = h0 + i * me.STEP + me.sub;
-      if (head >= cache.Hkv) continue;
-      const float s = __low2float(so[i]), o = __high2float(so[i]);
-      uint32_t out[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // code * scale is exact in fp32 (4 + 11 bits): one rounding of the sum, then bf16's
-        const float a = fmaf(whole((packed[i] >> (8 * j)) & 15u), s, o);
-        const float b = fmaf(whole((packed[i] >> (8 * j + 4)) & 15u), s, o);
-        const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-        out[j] = *reinterpret_cast<const uint32_t*>(&r);
-      }
-      *(reinterpret_cast<uint4*>(dst + (long long)head * D) + me.d8) =
-          make_uint4(out[0], out[1], out[2], out[3]);
+    if (++r == n) {
+      r = 0;
+      h0 += groups;
     }
+    const bool more = h0 < cache.Hkv;
+    if (more) load(r, h0);
+    if (owned) {
+      uint16_t* dst = (me.is_v ? v + row * v_stride : k + row * k_stride) + (head0 + me.sub) * D + 8 * me.d8;
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        if (head0 + i * me.STEP + me.sub >= cache.Hkv) continue;
+        uint32_t out[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // code * scale is exact in fp32 (4 + 11 bits): one rounding of the sum, then bf16's
+          const float a = fmaf(whole((packed[i] >> (8 * j)) & 15u), s[i], o[i]);
+          const float b = fmaf(whole((packed[i] >> (8 * j + 4)) & 15u), s[i], o[i]);
+          const __nv_bfloat162 y = __floats2bfloat162_rn(a, b);
+          out[j] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        *reinterpret_cast<uint4*>(dst + i * me.STEP * D) = make_uint4(out[0], out[1], out[2], out[3]);
+      }
+    }
+    if (!more) break;
   }
 }
 
-void grid_of(int64_t T, int Hkv, int D, cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr,
-             cudaStream_t s) {
-  const int rows = kThreads / 32, heads = kHeads * (D == 64 ? 2 : 1);
-  const int groups = (Hkv + heads - 1) / heads;
-  cfg->gridDim = dim3((unsigned)((T + rows - 1) / rows), (unsigned)(groups < 64 ? groups : 64));
+void grid_of(int64_t T, const Kv4Cache& c, int* run, cudaLaunchConfig_t* cfg,
+             cudaLaunchAttribute* attr, cudaStream_t s) {
+  const int heads = kHeads * (c.D == 64 ? 2 : 1);
+  const int groups = std::min((c.Hkv + heads - 1) / heads, 64);
+  const int64_t per_block = kThreads / 32, warps = (int64_t)num_sms() * 8 * per_block;
+  *run = (int)std::min<int64_t>(32, (T * groups + warps - 1) / warps);
+  const int64_t rows = *run * per_block;
+  cfg->gridDim = dim3((unsigned)((T + rows - 1) / rows), (unsigned)groups);
   cfg->blockDim = dim3(kThreads);
   cfg->stream = s;
   attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -280,10 +342,11 @@ cudaError_t launch_kv4_append(const uint16_t* k, int64_t k_stride, const uint16_
                               cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  grid_of(req.T, cache.Hkv, cache.D, &cfg, attr, s);
+  int run;
+  grid_of(req.T, cache, &run, &cfg, attr, s);
   auto kernel = cache.D == 64 ? kv4_append_kernel<64> : kv4_append_kernel<128>;
   return cudaLaunchKernelEx(&cfg, kernel, k, (long long)k_stride, v, (long long)v_stride, req,
-                            cache, err);
+                            cache, fast_div(cache.page), run, err);
 }
 
 cudaError_t launch_kv4_gather(const Kv4Req& req, const Kv4Cache& cache, uint16_t* k,
@@ -291,9 +354,10 @@ cudaError_t launch_kv4_gather(const Kv4Req& req, const Kv4Cache& cache, uint16_t
                               cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  grid_of(req.T, cache.Hkv, cache.D, &cfg, attr, s);
+  int run;
+  grid_of(req.T, cache, &run, &cfg, attr, s);
   auto kernel = cache.D == 64 ? kv4_gather_kernel<64> : kv4_gather_kernel<128>;
-  return cudaLaunchKernelEx(&cfg, kernel, req, cache, k, (long long)k_stride, v,
+  return cudaLaunchKernelEx(&cfg, kernel, req, cache, fast_div(cache.page), run, k, (long long)k_stride, v,
                             (long long)v_stride, err);
 }
 
