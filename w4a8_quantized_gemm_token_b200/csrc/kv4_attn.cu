@@ -38,14 +38,19 @@
 // the cut is between blocks, by kv4_join_kernel from the workspace, in the order
 // of the units: no atomics, the same bits on every run.
 //
-// One producer warp per block runs every consumer's ring of bulk copies (lane c
-// for consumer c): it walks the items, looks the pages up and keeps each ring
-// full.  The first copies of a span are issued by its consumer, a lane each.
+// A consumer copies its records itself, four ahead, with 16-byte asynchronous copies
+// of all its lanes.  What is slow about that, walking the items and looking the pages
+// up, is done by one producer warp per block (lane c for consumer c): it writes the
+// numbers of the next records, two windows of 32.  (With bulk copies issued by the
+// producer, a lane after the other, its issue was the limit: 109 cycles a record, 208 us
+// at 64 x 16384 with no arithmetic at all.)  A consumer works in runs of records that
+// are alike, so that a record's own work is in no loop with checks.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "fast_div.cuh"
 #include "kv4.cuh"
@@ -60,9 +65,12 @@ constexpr int kMaxBlocks = 160;  // a block per SM; the workspace holds this man
 template <int D, int NT>
 struct Cfg {
   static constexpr int ROWS = 8 * NT;
-  // NT = 1: 15 consumers and the producer, four warps to a quarter of the SM (128
-  // registers a thread); NT = 2: 11 and the producer, three warps (168 registers)
-  static constexpr int NW = NT == 1 ? 15 : 11;
+  // Consumers, beside the producer; the registers of the SM over four quarters.  D = 128:
+  // 11 (164 registers a thread used; 15 of 128 registers, 236 us against 231 at 64 x
+  // 16384), with two tiles 7 (255; 11 of 168 spill, 70 us against 62 at 4 x 2500, 200
+  // rows).  D = 64: 15 and 11, which spill nothing.
+  static constexpr int NW = D == 64 ? (NT == 1 ? 15 : 11) : (NT == 1 ? 11 : 7);
+  static constexpr int WINDOW = 32;                    // units a producer lane numbers at once
   static constexpr int STAGES = 4;                     // records in a consumer's ring
   static constexpr int THREADS = 32 * (NW + 1);
   static constexpr int LD = D + 4;                     // floats per row of a piece in shared memory
@@ -70,9 +78,9 @@ struct Cfg {
   static constexpr int RING = STAGES * Kv4<D>::REC;
   static constexpr int SM_RING = 0;
   static constexpr int SM_HEAD = SM_RING + NW * RING;  // piece of an item that began before the span
-  static constexpr int SM_BAR = SM_HEAD + NW * PIECE;  // full, empty per stage and consumer
-  static constexpr int SM_BAD = SM_BAR + NW * STAGES * 16;
-  static constexpr int SM_SPAN = (SM_BAD + NW * STAGES * 4 + 15) / 16 * 16;
+  static constexpr int SM_BAR = SM_HEAD + NW * PIECE;  // per consumer: window 0 and 1 full, empty
+  static constexpr int SM_IDX = SM_BAR + NW * 32;      // two windows of records' numbers
+  static constexpr int SM_SPAN = SM_IDX + NW * 2 * WINDOW * 4;
   static constexpr int SMEM = SM_SPAN + NW * 32 + 128;
   static_assert(PIECE <= RING, "a span's last piece is kept in its ring");
   static_assert(SM_HEAD % 16 == 0 && SM_BAR % 16 == 0 && SM_SPAN % 16 == 0, "alignment");
@@ -191,12 +199,41 @@ __device__ __forceinline__ long long request_units(const Args& a, const Item& ba
   return sum;
 }
 
+constexpr uint32_t kNoRecord = 0xFFFFFFFFu;
+
+// Record number (over the whole cache) of unit k of an item, from the id of its page.
+__device__ __forceinline__ int page_of(const Args& a, const Item& it, int k) {
+  return quot(record_of(it, k), a.by_page);
+}
+__device__ __forceinline__ int page_id(const Args& a, const Item& it, int k) {
+  if (it.p1 < 0) return 0;  // (an empty unit)
+  return __ldg(a.req.page_table + (long long)it.b * a.req.max_pages + page_of(a, it, k));
+}
+__device__ __forceinline__ uint32_t record_number(const Args& a, const Item& it, int k, int id) {
+  if (it.p1 < 0) return kNoRecord;
+  if (id < 0 || id >= a.cache.num_pages) {
+    record_index(a.err);
+    return kNoRecord;
+  }
+  const int in = record_of(it, k) - page_of(a, it, k) * a.by_page.d;
+  return ((uint32_t)id * (uint32_t)a.cache.Hkv + (uint32_t)it.kvh) * (uint32_t)a.by_page.d + (uint32_t)in;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // What a consumer warp starts from, in shared memory for its producer lane.
 struct Span {
-  long long units;
+  int units;
   int b, rt, kvh, k;
-  int filled;  // units whose copies the consumer has issued
-  int pad;
+  int filled;  // units that the consumer has numbered: at most a window, of its first item
+  int pad[2];
 };
 static_assert(sizeof(Span) == 32, "span size");
 
@@ -303,7 +340,7 @@ template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const Args a, int min_units) {
   using C = Cfg<D, NT>;
   using L = Kv4<D>;
-  constexpr int NG = L::NG, ROWS = C::ROWS, NW = C::NW, STAGES = C::STAGES;
+  constexpr int NG = L::NG, ROWS = C::ROWS, NW = C::NW, STAGES = C::STAGES, WINDOW = C::WINDOW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem<128>(smem_raw);
   __shared__ long long pre[C::THREADS + 1];
@@ -311,17 +348,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
   __shared__ long long tot[NW + 1];
   __shared__ int seg_flags[32];
   __shared__ int seg_item[NW][5];  // last piece's b, rt, kvh, row0, n
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int blk = blockIdx.x;
   const uint32_t bars = smem_u32(smem + C::SM_BAR);
-  auto full = [&](int w, int s) { return bars + (uint32_t)(w * STAGES + s) * 16u; };
-  auto empty = [&](int w, int s) { return full(w, s) + 8u; };
-  int* bad = reinterpret_cast<int*>(smem + C::SM_BAD);
+  auto full = [&](int w, int h) { return bars + (uint32_t)(w * 4 + h) * 8u; };
+  auto empty = [&](int w, int h) { return bars + (uint32_t)(w * 4 + 2 + h) * 8u; };
+  uint32_t* numbers = reinterpret_cast<uint32_t*>(smem + C::SM_IDX);
   Span* spans = reinterpret_cast<Span*>(smem + C::SM_SPAN);
 
-  if (threadIdx.x < NW * STAGES) {
-    mbar_init(full(0, threadIdx.x), 1);
-    mbar_init(empty(0, threadIdx.x), 1);
+  if (threadIdx.x < NW * 4) {
+    mbar_init(bars + threadIdx.x * 8u, 1);
     fence_mbar_init();
   }
   pdl_launch_dependents();
@@ -386,6 +422,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
 
   Item it = {};
   Span sp = {};
+  uint4 raw[NT][NG][2];  // this lane's query elements of a segment: row g, dims 16 t ..
+  auto load_queries = [&]() {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = it.rt * ROWS + 8 * n + g;
+      const int tok = quot(row, a.by_g);
+      const bool live = tok < it.n;
+      const uint16_t* src = a.q + (long long)(it.row0 + (live ? tok : 0)) * a.q_stride +
+                            (long long)(it.kvh * a.G + row - tok * a.G) * D + 16 * t;
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          raw[n][grp][j] = make_uint4(0, 0, 0, 0);
+          if (live) raw[n][grp][j] = *reinterpret_cast<const uint4*>(src + 64 * grp + 8 * j);
+        }
+    }
+  };
   if (warp < NW) {
     // ---- this warp's span of W / slots units (one more for the first W % slots), and
     // the item it starts in
@@ -393,7 +448,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
     const long long each = W >> 31 ? W / slots : (long long)((uint32_t)W / (uint32_t)slots);
     const int more = (int)(W - each * slots);
     const long long u0 = each * slot + min(slot, more);
-    sp.units = each + (slot < more ? 1 : 0);
+    const long long units = each + (slot < more ? 1 : 0);
+    const bool hours = units > 0x7FFFFF00ll;  // of work for one warp
+    if (hours) record_timeout(a.err);
+    sp.units = hours ? 0 : (int)units;
     if (sp.units > 0) {
       int lo = 0, hi = C::THREADS - 1;  // the last t with pre[t] <= u0: it has units
       while (lo < hi) {
@@ -447,23 +505,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
       sp.b = it.b;
       sp.rt = it.rt;
       sp.kvh = it.kvh;
-      if (it.p1 >= 0) sp.filled = (int)min((long long)min(STAGES, it.cnt - sp.k), sp.units);
-    }
-    // the first copies, a lane each
-    if (lane < sp.filled) {
-      const int rec_no = record_of(it, sp.k + lane), pg = quot(rec_no, a.by_page);
-      const int id = __ldg(a.req.page_table + (long long)it.b * a.req.max_pages + pg);
-      const bool fits = id >= 0 && id < a.cache.num_pages;
-      bad[warp * STAGES + lane] = fits ? 0 : 1;
-      if (fits) {
-        const long long rec = ((long long)id * a.cache.Hkv + it.kvh) * a.by_page.d + rec_no - pg * a.by_page.d;
-        mbar_arrive_expect_tx(full(warp, lane), L::REC);
-        bulk_load(smem_u32(smem + C::SM_RING + warp * C::RING + lane * L::REC),
-                  a.cache.base + rec * L::REC, L::REC, full(warp, lane));
-      } else {
-        record_index(a.err);
-        mbar_arrive(full(warp, lane));
-      }
+      sp.filled = min(min(WINDOW, it.cnt - sp.k), sp.units);
+      load_queries();
+      if (lane < sp.filled)
+        numbers[warp * 2 * WINDOW + lane] = record_number(a, it, sp.k + lane, page_id(a, it, sp.k + lane));
     }
     if (lane == 0) {
       spans[warp] = sp;
@@ -476,23 +521,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
 
   if (warp == NW) {
     // ------------------------------------------------------------- producer
-    long long left = 0, issued = 0;
-    int k = 0, s = 0;
-    uint32_t ph = 1;
+    int n = 0, units = 0, k = 0;  // units numbered; of the span; next unit of the item
     if (lane < NW) {
       const Span mine = spans[lane];
-      left = mine.units - mine.filled;
-      issued = mine.filled;
-      if (mine.filled == STAGES) {
-        ph = 0;
-      } else {
-        s = mine.filled;
-      }
-      if (left > 0) {
+      units = mine.units;
+      n = mine.filled;
+      if (units > 0 && (n == WINDOW || n == units)) mbar_arrive(full(lane, 0));
+      if (n < units) {
         it.b = mine.b;
         it.rt = mine.rt;
         it.kvh = mine.kvh;
-        k = mine.k + mine.filled;
+        k = mine.k + n;
         if (per == 1)
           set_request<ROWS>(a, it, seqs[it.b]);
         else
@@ -504,58 +543,33 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
         }
       }
     }
-    int rec_no = 0, pg = 0;
-    auto lookup = [&]() -> int {  // the next unit's record and page
-      if (left == 0 || it.p1 < 0) return -1;
-      rec_no = record_of(it, k);
-      pg = quot(rec_no, a.by_page);
-      return __ldg(a.req.page_table + (long long)it.b * a.req.max_pages + pg);
-    };
-    int id = lookup();
+    int id = n < units ? page_id(a, it, k) : 0;
     long long t0 = clock64();
-    while (__any_sync(0xFFFFFFFFu, left > 0)) {
+    while (__any_sync(0xFFFFFFFFu, n < units)) {
       bool moved = false;
-      if (left > 0 && mbar_test(empty(lane, s), ph)) {
+      // a window is written again once the consumer is done with it
+      if (n < units && (n < 2 * WINDOW || n % WINDOW != 0 ||
+                        mbar_test(empty(lane, n / WINDOW & 1), (uint32_t)(n / (2 * WINDOW) - 1) & 1u))) {
         moved = true;
-        const bool seen = it.p1 >= 0;
-        const bool fits = seen && id >= 0 && id < a.cache.num_pages;
-        if (seen && !fits) record_index(a.err);
-        bad[lane * STAGES + s] = fits ? 0 : 1;
-        if (fits) {
-          const long long rec = ((long long)id * a.cache.Hkv + it.kvh) * a.by_page.d + rec_no - pg * a.by_page.d;
-          mbar_arrive_expect_tx(full(lane, s), L::REC);
-          bulk_load(smem_u32(smem + C::SM_RING + lane * C::RING + s * L::REC),
-                    a.cache.base + rec * L::REC, L::REC, full(lane, s));
-        } else {
-          mbar_arrive(full(lane, s));
+        numbers[lane * 2 * WINDOW + n % (2 * WINDOW)] = record_number(a, it, k, id);
+        ++n;
+        if (n % WINDOW == 0 || n == units) mbar_arrive(full(lane, (n - 1) / WINDOW & 1));
+        if (n < units) {
+          if (++k == it.cnt) {
+            k = 0;
+            next_item<ROWS>(a, it);
+          }
+          id = page_id(a, it, k);
         }
-        ++issued;
-        if (++s == STAGES) {
-          s = 0;
-          ph ^= 1u;
-        }
-        --left;
-        if (left > 0 && ++k == it.cnt) {
-          k = 0;
-          next_item<ROWS>(a, it);
-        }
-        id = lookup();
       }
       if (__any_sync(0xFFFFFFFFu, moved)) {
         t0 = clock64();
       } else {
-        __nanosleep(64);  // leave the issue slots to the consumers
+        __nanosleep(256);  // leave the issue slots to the consumers
         if (clock64() - t0 > QK_WAIT_LIMIT_CYCLES) {
           if (lane == 0) record_timeout(a.err);
           break;
         }
-      }
-    }
-    // every copy has landed before the block may end
-    for (int j = 0; j < STAGES; ++j) {
-      if (lane < NW && issued > j) {
-        const long long u = issued - 1 - j;
-        mbar_wait(full(lane, (int)(u % STAGES)), (uint32_t)((u / STAGES) & 1), a.err);
       }
     }
   } else {
@@ -566,12 +580,41 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
     const uint8_t* ring_k = ring + (g * 4 + t) * 8 * NG;
     const uint8_t* ring_v = ring + L::V_OFF + (t * 8 + g) * 8 * NG;
     const uint8_t* ring_s = ring + L::KS_OFF + g * 4 * NG;
-    int k = sp.k, stage = 0;
-    uint32_t phase = 0;
+    int k = sp.k;
     bool first_piece = sp.k > 0;
     int flags = 0;
-    long long done = 0;
+    int done = 0;           // units worked on
+    int asked = 0;          // units whose copies are issued, or passed over
+    int known = sp.filled;  // units whose numbers are there
     bool ok = true;
+    const uint32_t* number = numbers + warp * 2 * WINDOW;
+    const uint8_t* cache = a.cache.base + 16 * lane;
+    const uint32_t ring_dst = smem_u32(ring) + 16 * lane;
+    // The numbers of unit `asked`'s window (false: the wait gave up).
+    auto know = [&]() {
+      if (asked < known || asked >= sp.units) return true;
+      known = asked / WINDOW * WINDOW + WINDOW;
+      return mbar_wait(full(warp, asked / WINDOW & 1), (uint32_t)(asked / (2 * WINDOW)) & 1u, a.err);
+    };
+    // A unit's copies into its place in the ring.
+    auto copy = [&](int unit, uint32_t place) {
+      const uint32_t rec = number[unit % (2 * WINDOW)];
+      const uint8_t* src = cache + (unsigned long long)rec * L::REC;
+      const uint32_t dst = ring_dst + place;
+      if (rec != kNoRecord) {
+#pragma unroll
+        for (int i = 0; i < L::REC / 512; ++i) copy16(dst + 512 * i, src + 512 * i);
+        if (lane < L::REC % 512 / 16) copy16(dst + L::REC / 512 * 512, src + L::REC / 512 * 512);
+      }
+    };
+    __syncwarp();
+#pragma unroll 1
+    for (; asked < STAGES && ok; ++asked) {
+      ok = know();
+      if (ok && asked < sp.units) copy(asked, asked * L::REC);
+      copies_commit();
+    }
+    uint32_t place = 0;  // of unit `done` in the ring, and then of unit `asked`
     while (done < sp.units && ok) {
       // ---- a segment: this span's units of one item
       // queries: fragments of row g (per j and half of a word's nibbles, the second
@@ -581,27 +624,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
       int pos[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int row = it.rt * ROWS + 8 * n + g;
-        const int tok = quot(row, a.by_g);
-        const bool live = tok < it.n;
-        const uint16_t* src = a.q + (long long)(it.row0 + (live ? tok : 0)) * a.q_stride +
-                              (long long)(it.kvh * a.G + row - tok * a.G) * D + 16 * t;
-        uint4 raw[NG][2];
         float top = 0.0f, sum[NG];
 #pragma unroll
         for (int grp = 0; grp < NG; ++grp) {
           sum[grp] = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            raw[grp][j] = make_uint4(0, 0, 0, 0);
-            if (live) raw[grp][j] = *reinterpret_cast<const uint4*>(src + 64 * grp + 8 * j);
-          }
         }
 #pragma unroll
         for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint32_t w[4] = {raw[grp][j].x, raw[grp][j].y, raw[grp][j].z, raw[grp][j].w};
+            const uint32_t w[4] = {raw[n][grp][j].x, raw[n][grp][j].y, raw[n][grp][j].z, raw[n][grp][j].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               sum[grp] += bf_lo(w[i]) + bf_hi(w[i]);
@@ -617,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
         for (int grp = 0; grp < NG; ++grp) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint4 v = raw[grp][j];
+            const uint4 v = raw[n][grp][j];
             qb[n][grp][j][0] = pack_f16(bf_lo(v.x) * f, bf_lo(v.z) * f);
             qb[n][grp][j][1] = pack_f16(bf_hi(v.x) * f * 0.0625f, bf_hi(v.z) * f * 0.0625f);
             qb[n][grp][j][2] = pack_f16(bf_lo(v.y) * f, bf_lo(v.w) * f);
@@ -673,36 +705,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
           for (int i = 0; i < 16; ++i) o[n][grp][i >> 3][(i >> 2) & 1][i & 3] *= alpha[i & 1];
       };
 
-      const long long room = sp.units - done;
-      const int stop = (long long)(it.cnt - k) <= room ? it.cnt : k + (int)room;
+      const int room = sp.units - done;
+      const int stop = it.cnt - k <= room ? it.cnt : k + room;
       const bool ends = stop == it.cnt;
-      done += stop - k;
-      for (; k < stop; ++k) {
-        const uint32_t bar = full(warp, stage);
-        if (!mbar_wait(bar, phase, a.err)) {
-          ok = false;
-          break;
-        }
-        const int at = stage * L::REC;
-        const int is_bad = bad[warp * STAGES + stage];
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-        if (is_bad) {  // nothing to see, or no such page
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar + 8u);
-          continue;
-        }
-
+      // A record: kMask where a row may not see all of its keys, dead where it is not there.
+      auto step = [&](auto masks, int record, bool dead, bool more) {
+        constexpr bool kMask = decltype(masks)::value;
+        copies_wait<STAGES - 1>();
+        __syncwarp();
+        const uint8_t* at_k = ring_k + place;
+        const uint8_t* at_v = ring_v + place;
+        const uint8_t* at_s = ring_s + place;
         // ---- scores: x[n][i], i = 0, 1 key g and rows 2 t, 2 t + 1; i = 2, 3 key g + 8
         float x[NT][4];
         {
           uint32_t k0[2 * NG], k1[2 * NG], s0[NG], s1[NG];
-          lds(k0, ring_k + at);
-          lds(k1, ring_k + at + 8 * 4 * 8 * NG);
-          lds(s0, ring_s + at);
-          lds(s1, ring_s + at + 8 * 4 * NG);
+          lds(k0, at_k);
+          lds(k1, at_k + 8 * 4 * 8 * NG);
+          lds(s0, at_s);
+          lds(s1, at_s + 8 * 4 * NG);
 #pragma unroll
           for (int grp = 0; grp < NG; ++grp) {
             float acc[NT][4];
@@ -712,15 +733,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
               for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              uint32_t u = k0[2 * grp + j], v = k1[2 * grp + j];
+              uint32_t c = k0[2 * grp + j], d = k1[2 * grp + j];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                  mma(acc[n], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
+                  mma(acc[n], c & 0x000F000Fu, d & 0x000F000Fu, c & 0x00F000F0u, d & 0x00F000F0u,
                       qb[n][grp][j][2 * h], qb[n][grp][j][2 * h + 1]);
-                u >>= 8;
-                v >>= 8;
+                c >>= 8;
+                d >>= 8;
               }
             }
             const float2 a0 = unpack_f16(s0[grp]), a1 = unpack_f16(s1[grp]);
@@ -734,34 +755,36 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
               }
           }
         }
-        const bool masked = k < it.whole0 || k >= it.whole1;
-        if (masked) {
-          const int key0 = (record_of(it, k) << 4) + g;
+        if constexpr (kMask) {
+          const int key0 = (record << 4) + g;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int key = key0 + 4 * (i & 2), p = pos[n][i & 1];
-              bool see = key <= p;
+              bool see = key <= p && !dead;
               if (a.window > 0) see = see && (key > p - a.window || key < a.sinks);
               if (!see) x[n][i] = -INFINITY;
             }
         }
-        // ---- values and their scales; the record is free then
+        // ---- values and their scales; the record's place is free then
         uint32_t v0[2 * NG], v1[2 * NG], t0[NG], t1[NG];
-        lds(v0, ring_v + at);
-        lds(v1, ring_v + at + 4 * 8 * 8 * NG);
-        lds(t0, ring_s + at + 16 * 4 * NG);
-        lds(t1, ring_s + at + 24 * 4 * NG);
+        lds(v0, at_v);
+        lds(v1, at_v + 4 * 8 * 8 * NG);
+        lds(t0, at_s + 16 * 4 * NG);
+        lds(t1, at_s + 24 * 4 * NG);
         __syncwarp();  // every lane has read the record
-        if (lane == 0) mbar_arrive(bar + 8u);
+        if (more) copy(asked, place);
+        copies_commit();
+        ++asked;
+        place = place == (STAGES - 1) * L::REC ? 0 : place + L::REC;
         // ---- a row's reference moves only where a score passes the last maximum by 2^4
         bool turn = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) turn |= fmaxf(x[n][c], x[n][2 + c]) > lim[n][c];
-        if (__any_sync(0xFFFFFFFFu, turn)) {
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, turn), 0)) {
           const float m0 = largest_scale(t0), m1 = largest_scale(t1);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
@@ -794,17 +817,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
             const float s0 = unpack_f16(t0[grp]).x, s1 = unpack_f16(t1[grp]).x;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              if (masked)
-                weigh<true>(x[n], s0, s1, w[n][grp]);
-              else
-                weigh<false>(x[n], s0, s1, w[n][grp]);
+              weigh<kMask>(x[n], s0, s1, w[n][grp]);
               big = __vmaxu2(big, __vmaxu2(w[n][grp][0], w[n][grp][1]));
             }
           }
           return big;
         };
         // a half of 2^15 or more carries into its sign bit
-        if (__any_sync(0xFFFFFFFFu, ((weights() + 0x08000800u) & 0x80008000u) != 0)) {
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, ((weights() + 0x08000800u) & 0x80008000u) != 0), 0)) {
           const float m0 = largest_scale(t0), m1 = largest_scale(t1);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
@@ -834,11 +854,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              if (masked)
-                off[n][c][grp] += (x[n][c] == 0.0f ? 0.0f : x[n][c] * o0) +
-                                  (x[n][2 + c] == 0.0f ? 0.0f : x[n][2 + c] * o1);
+              const float y0 = x[n][c], y1 = x[n][2 + c];
+              if (kMask)
+                off[n][c][grp] += (y0 == 0.0f ? 0.0f : y0 * o0) + (y1 == 0.0f ? 0.0f : y1 * o1);
               else
-                off[n][c][grp] = fmaf(x[n][c], o0, fmaf(x[n][2 + c], o1, off[n][c][grp]));
+                off[n][c][grp] = fmaf(y0, o0, fmaf(y1, o1, off[n][c][grp]));
             }
         }
 #pragma unroll
@@ -850,17 +870,46 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t u = v0[2 * grp + h], v = v1[2 * grp + h];
+            uint32_t c = v0[2 * grp + h], d = v1[2 * grp + h];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                mma(o[n][grp][h][i], u & 0x000F000Fu, u & 0x00F000F0u, v & 0x000F000Fu,
-                    v & 0x00F000F0u, w[n][grp][0], w[n][grp][1]);
-              u >>= 8;
-              v >>= 8;
+                mma(o[n][grp][h][i], c & 0x000F000Fu, c & 0x00F000F0u, d & 0x000F000Fu,
+                    d & 0x00F000F0u, w[n][grp][0], w[n][grp][1]);
+              c >>= 8;
+              d >>= 8;
             }
           }
+        }
+      };
+      while (k < stop) {
+        // a run of records alike: in one window of numbers, with the numbers of the
+        // units asked for known, and all masked or none
+        ok = know();
+        if (!ok) break;
+        const bool more = asked < sp.units;
+        int n = min(stop - k, WINDOW - done % WINDOW);
+        if (more) n = min(n, min(known, sp.units) - asked);
+        const bool whole = k >= it.whole0 && k < it.whole1;
+        if (whole) n = min(n, it.whole1 - k);
+        if (k < it.whole0) n = min(n, it.whole0 - k);
+        const uint32_t missing = __ballot_sync(0xFFFFFFFFu, number[(done / WINDOW * WINDOW + lane) % (2 * WINDOW)] == kNoRecord) >>
+                                 (done % WINDOW);
+        const bool dead = missing & 1u;
+        if (missing != 0) n = dead ? 1 : min(n, __ffs(missing) - 1);
+        const int end = k + n;
+        if (whole && !dead) {
+#pragma unroll 1
+          for (; k < end; ++k) step(std::false_type{}, 0, false, more);
+        } else {
+#pragma unroll 1
+          for (; k < end; ++k) step(std::true_type{}, record_of(it, k), dead, more);
+        }
+        done += n;
+        if (done % WINDOW == 0) {
+          __syncwarp();  // every lane is done with the window's numbers
+          if (lane == 0) mbar_arrive(empty(warp, (done / WINDOW - 1) & 1));
         }
       }
       if (!ok) break;
@@ -910,7 +959,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
           }
       } else {
         // a piece: an item's end or middle goes to the head slot, its beginning to the ring
-        // (whose copies have all been read: this is the span's last segment)
+        // (this is the span's last segment: nothing is in flight or unread)
         float* piece = reinterpret_cast<float*>(first_piece ? smem + C::SM_HEAD + warp * C::PIECE
                                                             : smem + C::SM_RING + warp * C::RING);
         __syncwarp();
@@ -946,8 +995,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
       if (ends && done < sp.units) {
         k = 0;
         next_item<ROWS>(a, it);
+        load_queries();
       }
     }
+    copies_wait<0>();  // (behind a wait that gave up)
     if (lane == 0) seg_flags[warp] = flags;
   }
   __syncthreads();

@@ -723,7 +723,8 @@ qk_status qk_rope(const uint16_t* q, int64_t q_stride, uint16_t* q_out, int64_t 
 // The cache's shape contract.
 static bool kv4_shape_ok(int64_t num_pages, int64_t Hkv, int64_t page, int64_t D) {
   return (D == 64 || D == 128) && page >= 16 && page <= 1024 && page % 16 == 0 && Hkv >= 1 &&
-         Hkv <= 65536 && num_pages >= 1 && num_pages <= INT32_MAX;
+         Hkv <= 65536 && num_pages >= 1 && num_pages <= INT32_MAX &&
+         num_pages * Hkv * (page / 16) < int64_t(UINT32_MAX);  // records have 32-bit numbers
 }
 
 // The arguments that the cache's three calls share.
