@@ -38,13 +38,12 @@
 // the cut is between blocks, by kv4_join_kernel from the workspace, in the order
 // of the units: no atomics, the same bits on every run.
 //
-// A consumer copies its records itself, four ahead, with 16-byte asynchronous copies
-// of all its lanes.  What is slow about that, walking the items and looking the pages
-// up, is done by one producer warp per block (lane c for consumer c): it writes the
-// numbers of the next records, two windows of 32.  (With bulk copies issued by the
-// producer, a lane after the other, its issue was the limit: 109 cycles a record, 208 us
-// at 64 x 16384 with no arithmetic at all.)  A consumer works in runs of records that
-// are alike, so that a record's own work is in no loop with checks.
+// A warp copies its records itself, four ahead, with 16-byte asynchronous copies of all
+// its lanes, and numbers them itself, 32 units at a time and a lane to a unit (the walk
+// over the items, the pages' ids).  It works in runs of records that are alike, so
+// that a record's own work is in no loop with checks.  (A producer warp that issued
+// bulk copies for the others, a lane after the other, took 109 cycles a record: 208 us
+// at 64 x 16384 with no arithmetic at all.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -65,25 +64,21 @@ constexpr int kMaxBlocks = 160;  // a block per SM; the workspace holds this man
 template <int D, int NT>
 struct Cfg {
   static constexpr int ROWS = 8 * NT;
-  // Consumers, beside the producer; the registers of the SM over four quarters.  D = 128:
-  // 11 (164 registers a thread used; 15 of 128 registers, 236 us against 231 at 64 x
-  // 16384), with two tiles 7 (255; 11 of 168 spill, 70 us against 62 at 4 x 2500, 200
-  // rows).  D = 64: 15 and 11, which spill nothing.
-  static constexpr int NW = D == 64 ? (NT == 1 ? 15 : 11) : (NT == 1 ? 11 : 7);
-  static constexpr int WINDOW = 32;                    // units a producer lane numbers at once
+  // Warps; the registers of the SM over four quarters.  D = 128: 12 of 168 registers, with
+  // two tiles 8 of 255 (12 spill); D = 64: 16 and 12.
+  static constexpr int NW = D == 64 ? (NT == 1 ? 16 : 12) : (NT == 1 ? 12 : 8);
+  static constexpr int WINDOW = 32;                    // units numbered at once
   static constexpr int STAGES = 4;                     // records in a consumer's ring
-  static constexpr int THREADS = 32 * (NW + 1);
+  static constexpr int THREADS = 32 * NW;
   static constexpr int LD = D + 4;                     // floats per row of a piece in shared memory
   static constexpr int PIECE = (ROWS * LD + 2 * ROWS) * 4;  // O rows, then m, l
   static constexpr int RING = STAGES * Kv4<D>::REC;
   static constexpr int SM_RING = 0;
   static constexpr int SM_HEAD = SM_RING + NW * RING;  // piece of an item that began before the span
-  static constexpr int SM_BAR = SM_HEAD + NW * PIECE;  // per consumer: window 0 and 1 full, empty
-  static constexpr int SM_IDX = SM_BAR + NW * 32;      // two windows of records' numbers
-  static constexpr int SM_SPAN = SM_IDX + NW * 2 * WINDOW * 4;
-  static constexpr int SMEM = SM_SPAN + NW * 32 + 128;
+  static constexpr int SM_IDX = SM_HEAD + NW * PIECE;  // two windows of records' numbers
+  static constexpr int SMEM = SM_IDX + NW * 2 * WINDOW * 4 + 128;
   static_assert(PIECE <= RING, "a span's last piece is kept in its ring");
-  static_assert(SM_HEAD % 16 == 0 && SM_BAR % 16 == 0 && SM_SPAN % 16 == 0, "alignment");
+  static_assert(SM_HEAD % 16 == 0 && SM_IDX % 16 == 0, "alignment");
   static_assert(SMEM + 24 * (THREADS + 64) <= 232448, "with the static shared memory");
 };
 
@@ -104,9 +99,11 @@ struct Args {
 // ---- workspace: header, a word per block, then two pieces per block (its first
 // item's, where that began in an earlier block, and its last's)
 struct Meta {
-  int flags;  // 1: a first piece, 2: it ends its item, 4: a last piece (of item b, rt, kvh)
-  int b, rt, kvh;
+  int flags;  // 1: a first piece, 2: it ends its item, 4: a last piece, of
+  int rt, kvh, row0, n;  // this row tile and kv head of the request with these rows
+  int pad[3];
 };
+static_assert(sizeof(Meta) == 32, "read as two 16-byte words");
 constexpr size_t kMetaOff = 256;
 constexpr size_t kPieceOff = kMetaOff + kMaxBlocks * sizeof(Meta);
 __host__ __device__ constexpr size_t piece_floats(int D) { return (size_t)16 * (D + 2); }
@@ -228,31 +225,10 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// What a consumer warp starts from, in shared memory for its producer lane.
-struct Span {
-  int units;
-  int b, rt, kvh, k;
-  int filled;  // units that the consumer has numbered: at most a window, of its first item
-  int pad[2];
-};
-static_assert(sizeof(Span) == 32, "span size");
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 
 // D += A B, 16 x 8 x 16, fp16 operands, fp32 sums.
@@ -345,21 +321,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
   uint8_t* smem = align_smem<128>(smem_raw);
   __shared__ long long pre[C::THREADS + 1];
   __shared__ Kv4Seq seqs[C::THREADS];
-  __shared__ long long tot[NW + 1];
+  __shared__ long long tot[NW];
   __shared__ int seg_flags[32];
-  __shared__ int seg_item[NW][5];  // last piece's b, rt, kvh, row0, n
+  __shared__ __align__(16) int seg_item[NW][4];  // last piece's rt, kvh, row0, n
+  __shared__ __align__(16) int ahead[NW][4];     // the next unit to be numbered: b, rt, kvh, unit of the item
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int blk = blockIdx.x;
-  const uint32_t bars = smem_u32(smem + C::SM_BAR);
-  auto full = [&](int w, int h) { return bars + (uint32_t)(w * 4 + h) * 8u; };
-  auto empty = [&](int w, int h) { return bars + (uint32_t)(w * 4 + 2 + h) * 8u; };
-  uint32_t* numbers = reinterpret_cast<uint32_t*>(smem + C::SM_IDX);
-  Span* spans = reinterpret_cast<Span*>(smem + C::SM_SPAN);
+  uint32_t* number = reinterpret_cast<uint32_t*>(smem + C::SM_IDX) + warp * 2 * WINDOW;
 
-  if (threadIdx.x < NW * 4) {
-    mbar_init(bars + threadIdx.x * 8u, 1);
-    fence_mbar_init();
-  }
   pdl_launch_dependents();
   pdl_wait();
 
@@ -421,7 +390,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
   if (blk >= blocks) return;  // the whole block
 
   Item it = {};
-  Span sp = {};
+  int units = 0, k = 0;  // of this warp's span; the unit of the item that it begins with
   uint4 raw[NT][NG][2];  // this lane's query elements of a segment: row g, dims 16 t ..
   auto load_queries = [&]() {
     const int g = lane >> 2, t = lane & 3;
@@ -441,18 +410,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
         }
     }
   };
-  if (warp < NW) {
+  {
     // ---- this warp's span of W / slots units (one more for the first W % slots), and
     // the item it starts in
     const int slot = blk * NW + warp, slots = blocks * NW;
     const long long each = W >> 31 ? W / slots : (long long)((uint32_t)W / (uint32_t)slots);
     const int more = (int)(W - each * slots);
     const long long u0 = each * slot + min(slot, more);
-    const long long units = each + (slot < more ? 1 : 0);
-    const bool hours = units > 0x7FFFFF00ll;  // of work for one warp
+    const long long all = each + (slot < more ? 1 : 0);
+    const bool hours = all > 0x7FFFFF00ll;  // of work for one warp
     if (hours) record_timeout(a.err);
-    sp.units = hours ? 0 : (int)units;
-    if (sp.units > 0) {
+    units = hours ? 0 : (int)all;
+    if (units > 0) {
       int lo = 0, hi = C::THREADS - 1;  // the last t with pre[t] <= u0: it has units
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -494,107 +463,64 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
         }
         rest -= __shfl_sync(0xFFFFFFFFu, sum, 31);
         if (rt0 + 32 >= it.nrt) {  // not reached: the units add up
-          sp.units = 0;
+          units = 0;
           break;
         }
       }
       it.rt = at;
       load_tile<ROWS>(a, it);
       it.kvh = rest >> 31 ? (int)(rest / it.cnt) : (int)((uint32_t)rest / (uint32_t)it.cnt);
-      sp.k = (int)(rest - (long long)it.kvh * it.cnt);
-      sp.b = it.b;
-      sp.rt = it.rt;
-      sp.kvh = it.kvh;
-      sp.filled = min(min(WINDOW, it.cnt - sp.k), sp.units);
+      k = (int)(rest - (long long)it.kvh * it.cnt);
       load_queries();
-      if (lane < sp.filled)
-        numbers[warp * 2 * WINDOW + lane] = record_number(a, it, sp.k + lane, page_id(a, it, sp.k + lane));
+      if (lane == 0) *reinterpret_cast<int4*>(ahead[warp]) = make_int4(it.b, it.rt, it.kvh, k);
     }
-    if (lane == 0) {
-      spans[warp] = sp;
-      seg_flags[warp] = 0;
-    }
-  } else if (lane >= NW) {
-    seg_flags[lane] = 0;
   }
-  __syncthreads();
 
-  if (warp == NW) {
-    // ------------------------------------------------------------- producer
-    int n = 0, units = 0, k = 0;  // units numbered; of the span; next unit of the item
-    if (lane < NW) {
-      const Span mine = spans[lane];
-      units = mine.units;
-      n = mine.filled;
-      if (units > 0 && (n == WINDOW || n == units)) mbar_arrive(full(lane, 0));
-      if (n < units) {
-        it.b = mine.b;
-        it.rt = mine.rt;
-        it.kvh = mine.kvh;
-        k = mine.k + n;
-        if (per == 1)
-          set_request<ROWS>(a, it, seqs[it.b]);
-        else
-          load_request<ROWS>(a, it);
-        load_tile<ROWS>(a, it);
-        if (k == it.cnt) {
-          k = 0;
-          next_item<ROWS>(a, it);
-        }
-      }
-    }
-    int id = n < units ? page_id(a, it, k) : 0;
-    long long t0 = clock64();
-    while (__any_sync(0xFFFFFFFFu, n < units)) {
-      bool moved = false;
-      // a window is written again once the consumer is done with it
-      if (n < units && (n < 2 * WINDOW || n % WINDOW != 0 ||
-                        mbar_test(empty(lane, n / WINDOW & 1), (uint32_t)(n / (2 * WINDOW) - 1) & 1u))) {
-        moved = true;
-        numbers[lane * 2 * WINDOW + n % (2 * WINDOW)] = record_number(a, it, k, id);
-        ++n;
-        if (n % WINDOW == 0 || n == units) mbar_arrive(full(lane, (n - 1) / WINDOW & 1));
-        if (n < units) {
-          if (++k == it.cnt) {
-            k = 0;
-            next_item<ROWS>(a, it);
-          }
-          id = page_id(a, it, k);
-        }
-      }
-      if (__any_sync(0xFFFFFFFFu, moved)) {
-        t0 = clock64();
-      } else {
-        __nanosleep(256);  // leave the issue slots to the consumers
-        if (clock64() - t0 > QK_WAIT_LIMIT_CYCLES) {
-          if (lane == 0) record_timeout(a.err);
-          break;
-        }
-      }
-    }
-  } else {
-    // ------------------------------------------------------------ consumers
+  {
     const int g = lane >> 2, t = lane & 3;
     const uint8_t* ring = smem + C::SM_RING + warp * C::RING;
     // this lane's places in a record: codes of tokens g, g + 8; of pairs t, t + 4
     const uint8_t* ring_k = ring + (g * 4 + t) * 8 * NG;
     const uint8_t* ring_v = ring + L::V_OFF + (t * 8 + g) * 8 * NG;
     const uint8_t* ring_s = ring + L::KS_OFF + g * 4 * NG;
-    int k = sp.k;
-    bool first_piece = sp.k > 0;
+    bool first_piece = k > 0;
     int flags = 0;
-    int done = 0;           // units worked on
-    int asked = 0;          // units whose copies are issued, or passed over
-    int known = sp.filled;  // units whose numbers are there
-    bool ok = true;
-    const uint32_t* number = numbers + warp * 2 * WINDOW;
+    int done = 0;   // units worked on
+    int asked = 0;  // units whose copies are issued, or passed over
+    int known = 0;  // units that are numbered
     const uint8_t* cache = a.cache.base + 16 * lane;
     const uint32_t ring_dst = smem_u32(ring) + 16 * lane;
-    // The numbers of unit `asked`'s window (false: the wait gave up).
-    auto know = [&]() {
-      if (asked < known || asked >= sp.units) return true;
-      known = asked / WINDOW * WINDOW + WINDOW;
-      return mbar_wait(full(warp, asked / WINDOW & 1), (uint32_t)(asked / (2 * WINDOW)) & 1u, a.err);
+    // Numbers the next window of units, a lane each; the units of one item look their
+    // pages up together.
+    auto number_more = [&]() {
+      __syncwarp();
+      const int4 from = *reinterpret_cast<const int4*>(ahead[warp]);
+      Item at;
+      at.b = from.x;
+      at.rt = from.y;
+      at.kvh = from.z;
+      int u = from.w, have = 0;
+      if (per == 1)
+        set_request<ROWS>(a, at, seqs[at.b]);
+      else
+        load_request<ROWS>(a, at);
+      load_tile<ROWS>(a, at);
+      const int want = min(WINDOW, units - known);
+      uint32_t mine = kNoRecord;
+      while (have < want) {
+        const int n = min(want - have, at.cnt - u), e = u + lane - have;
+        if (lane >= have && lane < have + n) mine = record_number(a, at, e, page_id(a, at, e));
+        have += n;
+        u += n;
+        if (u == at.cnt && known + have < units) {
+          u = 0;
+          next_item<ROWS>(a, at);
+        }
+      }
+      number[(known + lane) % (2 * WINDOW)] = mine;
+      known += want;
+      __syncwarp();
+      if (lane == 0) *reinterpret_cast<int4*>(ahead[warp]) = make_int4(at.b, at.rt, at.kvh, u);
     };
     // A unit's copies into its place in the ring.
     auto copy = [&](int unit, uint32_t place) {
@@ -607,15 +533,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
         if (lane < L::REC % 512 / 16) copy16(dst + L::REC / 512 * 512, src + L::REC / 512 * 512);
       }
     };
-    __syncwarp();
+    if (units > 0) number_more();
 #pragma unroll 1
-    for (; asked < STAGES && ok; ++asked) {
-      ok = know();
-      if (ok && asked < sp.units) copy(asked, asked * L::REC);
+    for (; asked < STAGES; ++asked) {
+      if (asked < units) copy(asked, asked * L::REC);
       copies_commit();
     }
     uint32_t place = 0;  // of unit `done` in the ring, and then of unit `asked`
-    while (done < sp.units && ok) {
+    while (done < units) {
       // ---- a segment: this span's units of one item
       // queries: fragments of row g (per j and half of a word's nibbles, the second
       // of a pair a 16th); sums and factors of rows 2 t, 2 t + 1, the columns of the scores
@@ -705,7 +630,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
           for (int i = 0; i < 16; ++i) o[n][grp][i >> 3][(i >> 2) & 1][i & 3] *= alpha[i & 1];
       };
 
-      const int room = sp.units - done;
+      const int room = units - done;
       const int stop = it.cnt - k <= room ? it.cnt : k + room;
       const bool ends = stop == it.cnt;
       // A record: kMask where a row may not see all of its keys, dead where it is not there.
@@ -886,11 +811,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
       while (k < stop) {
         // a run of records alike: in one window of numbers, with the numbers of the
         // units asked for known, and all masked or none
-        ok = know();
-        if (!ok) break;
-        const bool more = asked < sp.units;
+        const bool more = asked < units;
+        if (more && asked == known) number_more();
         int n = min(stop - k, WINDOW - done % WINDOW);
-        if (more) n = min(n, min(known, sp.units) - asked);
+        if (more) n = min(n, known - asked);
         const bool whole = k >= it.whole0 && k < it.whole1;
         if (whole) n = min(n, it.whole1 - k);
         if (k < it.whole0) n = min(n, it.whole0 - k);
@@ -907,13 +831,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
           for (; k < end; ++k) step(std::true_type{}, record_of(it, k), dead, more);
         }
         done += n;
-        if (done % WINDOW == 0) {
-          __syncwarp();  // every lane is done with the window's numbers
-          if (lane == 0) mbar_arrive(empty(warp, (done / WINDOW - 1) & 1));
-        }
       }
-      if (!ok) break;
-
       // ---- the segment's sums: l and the offsets' part over the lanes of a row; then
       // z = O of row 2 t + c, dims 64 group + 8 g + 4 h + 2 i + (0, 1)
 #pragma unroll
@@ -982,24 +900,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
             }
           }
         if (lane == 0 && !first_piece) {
-          int* id = seg_item[warp];
-          id[0] = it.b;
-          id[1] = it.rt;
-          id[2] = it.kvh;
-          id[3] = it.row0;
-          id[4] = it.n;
+          *reinterpret_cast<int4*>(seg_item[warp]) = make_int4(it.rt, it.kvh, it.row0, it.n);
         }
         flags |= first_piece ? (ends ? 3 : 1) : 4;
       }
       first_piece = false;
-      if (ends && done < sp.units) {
+      if (ends && done < units) {
         k = 0;
         next_item<ROWS>(a, it);
         load_queries();
       }
     }
-    copies_wait<0>();  // (behind a wait that gave up)
     if (lane == 0) seg_flags[warp] = flags;
+    if (warp == 0 && lane >= NW) seg_flags[lane] = 0;
   }
   __syncthreads();
 
@@ -1009,54 +922,74 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
   const uint32_t heads = __ballot_sync(0xFFFFFFFFu, my_flags & 1);
   const uint32_t end_at = __ballot_sync(0xFFFFFFFFu, my_flags & 2);
   const uint32_t tails = __ballot_sync(0xFFFFFFFFu, my_flags & 4);
-  Meta meta = {0, 0, 0, 0};
+  Meta meta = {};
+  // One row of a chain to a warp (D = 64: to half of one): the weights of all pieces, a
+  // lane to a piece, then the pieces in turn.
+  constexpr int LPR = D / 4, RPW = 32 / LPR;
+  int next = 0;  // the warp whose turn it is
   auto emit = [&](int start, uint32_t parts, bool ended) {
     const bool whole = start >= 0 && ended;
-    float* part = nullptr;
+    float* part = piece_at(a.ws, D, blk, start >= 0 ? 1 : 0);
+    int4 item = make_int4(0, 0, 0, 0);
+    if (start >= 0) item = *reinterpret_cast<const int4*>(seg_item[start]);
     if (!whole) {
-      part = piece_at(a.ws, D, blk, start >= 0 ? 1 : 0);
+      meta.flags |= start >= 0 ? 4 : ended ? 3 : 1;
       if (start >= 0) {
-        meta.flags |= 4;
-        meta.b = seg_item[start][0];
-        meta.rt = seg_item[start][1];
-        meta.kvh = seg_item[start][2];
-      } else {
-        meta.flags |= ended ? 3 : 1;
+        meta.rt = item.x;
+        meta.kvh = item.y;
+        meta.row0 = item.z;
+        meta.n = item.w;
       }
     }
     const float* first = reinterpret_cast<const float*>(smem + C::SM_RING + max(start, 0) * C::RING);
     const float* rest = reinterpret_cast<const float*>(smem + C::SM_HEAD);
-    for (int e = threadIdx.x; e < ROWS * (D / 4); e += C::THREADS) {
-      const int r = e / (D / 4), d = 4 * (e % (D / 4));
-      // weights of all pieces first, so that their loads do not wait for one another
-      float wt[NW], own = kLeast, top = kLeast;
+    for (int r0 = 0; r0 < ROWS; r0 += RPW) {
+      const bool mine = next == warp;
+      next = next == NW - 1 ? 0 : next + 1;
+      if (!mine) continue;
+      const int r = r0 + lane / LPR, d = 4 * (lane % LPR);
+      static_assert(NW < 32, "lane p holds piece p's weight, lane 31 the chain's first one's");
+      const float* p = lane == 31 ? first : rest + min(lane, NW - 1) * (C::PIECE / 4);
+      const bool has = lane == 31 ? start >= 0 : lane < NW && ((parts >> lane) & 1u);
+      float wt[RPW], top = kLeast, sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        wt[w] = (parts >> w) & 1u ? rest[w * (C::PIECE / 4) + ROWS * C::LD + r] : kLeast;
-        top = fmaxf(top, wt[w]);
+      for (int h = 0; h < RPW; ++h) {
+        const float m = has ? p[ROWS * C::LD + r0 + h] : kLeast;
+        float most = m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+        wt[h] = has ? ex2(m - most) : 0.0f;
+        float all = has ? wt[h] * p[ROWS * C::LD + ROWS + r0 + h] : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+        if (lane / LPR == h) {
+          top = most;
+          sum = all;
+        }
       }
-      if (start >= 0) own = first[ROWS * C::LD + r];
-      top = fmaxf(top, own);
-      float sum = 0.0f;
       float4 v = make_float4(0, 0, 0, 0);
-      auto add = [&](const float* p, float f) {
-        sum = fmaf(f, p[ROWS * C::LD + ROWS + r], sum);
+      auto add = [&](const float* p, int from) {
+        float f = __shfl_sync(0xFFFFFFFFu, wt[0], from);
+#pragma unroll
+        for (int h = 1; h < RPW; ++h) {
+          const float other = __shfl_sync(0xFFFFFFFFu, wt[h], from);
+          f = lane / LPR == h ? other : f;
+        }
         const float4 x = *reinterpret_cast<const float4*>(p + r * C::LD + d);
         v.x = fmaf(f, x.x, v.x);
         v.y = fmaf(f, x.y, v.y);
         v.z = fmaf(f, x.z, v.z);
         v.w = fmaf(f, x.w, v.w);
       };
-      if (start >= 0) add(first, ex2(own - top));
+      if (start >= 0) add(first, 31);
 #pragma unroll
       for (int w = 0; w < NW; ++w)
-        if ((parts >> w) & 1u) add(rest + w * (C::PIECE / 4), ex2(wt[w] - top));
+        if ((parts >> w) & 1u) add(rest + w * (C::PIECE / 4), w);
       if (whole) {
-        const int row = seg_item[start][1] * ROWS + r, tok = quot(row, a.by_g);
-        if (tok < seg_item[start][4]) {
+        const int row = item.x * ROWS + r, tok = quot(row, a.by_g);
+        if (tok < item.w) {
           const float inv = sum > 0.0f ? 1.0f / sum : sum;
-          uint16_t* dst = a.out + ((long long)(seg_item[start][3] + tok) * a.H + seg_item[start][2] * a.G +
-                                   row - tok * a.G) * D + d;
+          uint16_t* dst = a.out + ((long long)(item.z + tok) * a.H + item.y * a.G + row - tok * a.G) * D + d;
           *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
         }
       } else {
@@ -1071,32 +1004,35 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
   int start = -1;       // the chain's last piece; -1: it began in an earlier block
   uint32_t parts = 0;   // its first pieces
   bool open = heads != 0 && (tails & ((heads & (0u - heads)) - 1u)) == 0;
-  for (int w = 0; w < NW; ++w) {
-    if ((heads >> w) & 1u) {
-      parts |= 1u << w;
-      if ((end_at >> w) & 1u) {
-        if (open) emit(start, parts, true);
-        open = false;
-        parts = 0;
-      }
+#pragma unroll 1
+  for (int w = 0; w <= NW; ++w) {
+    const uint32_t bit = w < NW ? 1u << w : 0u;
+    parts |= heads & bit;
+    const bool ended = (heads & end_at & bit) != 0;
+    if (open && (ended || w == NW)) emit(start, parts, ended);
+    if (ended) {
+      open = false;
+      parts = 0;
     }
-    if ((tails >> w) & 1u) {
+    if (tails & bit) {
       start = w;
       parts = 0;
       open = true;
     }
   }
-  if (open) emit(start, parts, false);
   if (threadIdx.x == 0) reinterpret_cast<Meta*>(a.ws + kMetaOff)[blk] = meta;
 }
 
 // Joins the items that are cut between blocks: block (c, row) the one whose
 // beginning is block c's last piece, with the first pieces of the blocks behind it.
 // D / 4 threads read a piece's row; the 512 / D groups of them take the pieces in turn.
+// A launch waits for two loads, one after the other: every block's Meta, and then
+// the pieces' rows with their maxima and sums.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(128) kv4_join_kernel(const Args a) {
-  constexpr int TPP = D / 4, GROUPS = 128 / TPP;
-  __shared__ float weight[kMaxBlocks + 1];
+  constexpr int TPP = D / 4, GROUPS = 128 / TPP, AHEAD = 4;
+  __shared__ int flags[kMaxBlocks];
+  __shared__ float weight[kMaxBlocks];
   __shared__ __align__(16) float red[GROUPS][D];
   __shared__ float total;
   pdl_launch_dependents();
@@ -1104,14 +1040,16 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Args a) {
   const int c = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31;
   const int blocks = *reinterpret_cast<const int*>(a.ws);
   const Meta* meta = reinterpret_cast<const Meta*>(a.ws + kMetaOff);
-  if (c >= blocks) return;
   const Meta me = meta[c];
-  if (!(me.flags & 4)) return;
+  // (Metas behind the last block are not written, and not looked at)
+  for (int e = threadIdx.x; e < gridDim.x; e += 128) flags[e] = meta[e].flags;
+  if (c >= blocks || !(me.flags & 4)) return;
+  __syncthreads();
   // the chain: blocks c + 1 .. last (a block with no first piece in it has no units)
   int last = blocks - 1;
   for (int e0 = c + 1; e0 < blocks; e0 += 32) {
     const int e = e0 + lane;
-    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, e < blocks && (meta[e].flags & 2) != 0);
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, e < blocks && (flags[e] & 2) != 0);
     if (hit != 0) {
       last = e0 + __ffs(hit) - 1;
       break;
@@ -1119,55 +1057,68 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Args a) {
   }
   const int n = last - c + 1;
   auto piece = [&](int i) { return piece_at(a.ws, D, c + i, i == 0 ? 1 : 0); };
+  auto has = [&](int i) { return i < n && (i == 0 || (flags[c + i] & 1) != 0); };
+  const int grp = threadIdx.x / TPP, d = 4 * (threadIdx.x % TPP);
+  float4 x[AHEAD];
+#pragma unroll
+  for (int j = 0; j < AHEAD; ++j) {
+    const int i = grp + j * GROUPS;
+    x[j] = make_float4(0, 0, 0, 0);
+    if (has(i)) x[j] = *reinterpret_cast<const float4*>(piece(i) + r * D + d);
+  }
   if (threadIdx.x < 32) {
-    float top = kLeast;
-    for (int i = lane; i < n; i += 32) {
-      const bool has = i == 0 || (meta[c + i].flags & 1) != 0;
-      const float m = has ? piece(i)[16 * D + r] : kLeast;
-      weight[i] = has ? m : -INFINITY;
-      top = fmaxf(top, m);
+    constexpr int PER = (kMaxBlocks + 31) / 32;
+    float m[PER], l[PER], top = kLeast, sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = lane + 32 * j;
+      m[j] = has(i) ? piece(i)[16 * D + r] : kLeast;
+      l[j] = has(i) ? piece(i)[16 * D + 16 + r] : 0.0f;
+      top = fmaxf(top, m[j]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    float sum = 0.0f;
-    for (int i = lane; i < n; i += 32) {
-      const float f = ex2(weight[i] - top);
-      weight[i] = f;
-      if (f != 0.0f) sum = fmaf(f, piece(i)[16 * D + 16 + r], sum);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = lane + 32 * j;
+      const float f = has(i) ? ex2(m[j] - top) : 0.0f;
+      if (i < n) weight[i] = f;
+      if (f != 0.0f) sum = fmaf(f, l[j], sum);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane == 0) total = sum;
   }
   __syncthreads();
-  const int grp = threadIdx.x / TPP, d = 4 * (threadIdx.x % TPP);
   float4 v = make_float4(0, 0, 0, 0);
+  auto add = [&](int i, const float4& y) {
+    const float f = i < n ? weight[i] : 0.0f;
+    if (f == 0.0f) return;
+    v.x = fmaf(f, y.x, v.x);
+    v.y = fmaf(f, y.y, v.y);
+    v.z = fmaf(f, y.z, v.z);
+    v.w = fmaf(f, y.w, v.w);
+  };
+#pragma unroll
+  for (int j = 0; j < AHEAD; ++j) add(grp + j * GROUPS, x[j]);
 #pragma unroll 4
-  for (int i = grp; i < n; i += GROUPS) {
-    const float f = weight[i];
-    if (f == 0.0f) continue;
-    const float4 x = *reinterpret_cast<const float4*>(piece(i) + r * D + d);
-    v.x = fmaf(f, x.x, v.x);
-    v.y = fmaf(f, x.y, v.y);
-    v.z = fmaf(f, x.z, v.z);
-    v.w = fmaf(f, x.w, v.w);
-  }
+  for (int i = grp + AHEAD * GROUPS; i < n; i += GROUPS)
+    if (has(i)) add(i, *reinterpret_cast<const float4*>(piece(i) + r * D + d));
   *reinterpret_cast<float4*>(&red[grp][d]) = v;
   __syncthreads();
   if (threadIdx.x >= TPP) return;
 #pragma unroll
   for (int i = 1; i < GROUPS; ++i) {
-    const float4 x = *reinterpret_cast<const float4*>(&red[i][d]);
-    v.x += x.x;
-    v.y += x.y;
-    v.z += x.z;
-    v.w += x.w;
+    const float4 y = *reinterpret_cast<const float4*>(&red[i][d]);
+    v.x += y.x;
+    v.y += y.y;
+    v.z += y.z;
+    v.w += y.w;
   }
-  const Kv4Seq sq = kv4_seq(a.req, me.b, a.err);
   const int row = me.rt * ROWS + r, tok = quot(row, a.by_g);
-  if (tok >= sq.n) return;
+  if (tok >= me.n) return;
   const float sum = total, inv = sum > 0.0f ? 1.0f / sum : sum;
-  uint16_t* dst = a.out + ((long long)(sq.row0 + tok) * a.H + me.kvh * a.G + row - tok * a.G) * D + d;
+  uint16_t* dst = a.out + ((long long)(me.row0 + tok) * a.H + me.kvh * a.G + row - tok * a.G) * D + d;
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
 }
 
