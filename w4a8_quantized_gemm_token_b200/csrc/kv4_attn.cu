@@ -71,7 +71,7 @@ struct Cfg {
   static constexpr int STAGES = 4;                     // records in a consumer's ring
   static constexpr int THREADS = 32 * NW;
   static constexpr int LD = D + 4;                     // floats per row of a piece in shared memory
-  static constexpr int PIECE = (ROWS * LD + 2 * ROWS) * 4;  // O rows, then m, l
+  static constexpr int PIECE = (ROWS * LD + 2 * ROWS) * 4;  // O rows, then every row's (m, l)
   static constexpr int RING = STAGES * Kv4<D>::REC;
   static constexpr int SM_RING = 0;
   static constexpr int SM_HEAD = SM_RING + NW * RING;  // piece of an item that began before the span
@@ -422,11 +422,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
     if (hours) record_timeout(a.err);
     units = hours ? 0 : (int)all;
     if (units > 0) {
-      int lo = 0, hi = C::THREADS - 1;  // the last t with pre[t] <= u0: it has units
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pre[mid] <= u0) lo = mid; else hi = mid - 1;
-      }
+      // the last t with pre[t] <= u0 (it has units): among every NW-th, then among those
+      // behind it
+      int lo = (__popc(__ballot_sync(0xFFFFFFFFu, pre[lane * NW] <= u0)) - 1) * NW;
+      lo += __popc(__ballot_sync(0xFFFFFFFFu, lane < NW && pre[lo + min(lane, NW - 1)] <= u0)) - 1;
       long long rest = u0 - pre[lo];
       it.b = lo * per;
       set_request<ROWS>(a, it, seqs[lo]);
@@ -895,8 +894,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
                     make_float4(o[n][grp][h][0][c], o[n][grp][h][0][2 + c], o[n][grp][h][1][c],
                                 o[n][grp][h][1][2 + c]);
             if (g == 0) {
-              piece[ROWS * C::LD + row] = -nm[n][c];
-              piece[ROWS * C::LD + ROWS + row] = l[n][c];
+              *reinterpret_cast<float2*>(piece + ROWS * C::LD + 2 * row) = make_float2(-nm[n][c], l[n][c]);
             }
           }
         if (lane == 0 && !first_piece) {
@@ -923,8 +921,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
   const uint32_t end_at = __ballot_sync(0xFFFFFFFFu, my_flags & 2);
   const uint32_t tails = __ballot_sync(0xFFFFFFFFu, my_flags & 4);
   Meta meta = {};
-  // One row of a chain to a warp (D = 64: to half of one): the weights of all pieces, a
-  // lane to a piece, then the pieces in turn.
+  // One row of a chain to a warp (D = 64: to half of one), all pieces' loads at once.
   constexpr int LPR = D / 4, RPW = 32 / LPR;
   int next = 0;  // the warp whose turn it is
   auto emit = [&](int start, uint32_t parts, bool ended) {
@@ -948,43 +945,33 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
       next = next == NW - 1 ? 0 : next + 1;
       if (!mine) continue;
       const int r = r0 + lane / LPR, d = 4 * (lane % LPR);
-      static_assert(NW < 32, "lane p holds piece p's weight, lane 31 the chain's first one's");
-      const float* p = lane == 31 ? first : rest + min(lane, NW - 1) * (C::PIECE / 4);
-      const bool has = lane == 31 ? start >= 0 : lane < NW && ((parts >> lane) & 1u);
-      float wt[RPW], top = kLeast, sum = 0.0f;
+      float4 x[NW + 1];
+      float2 ml[NW + 1];
 #pragma unroll
-      for (int h = 0; h < RPW; ++h) {
-        const float m = has ? p[ROWS * C::LD + r0 + h] : kLeast;
-        float most = m;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-        wt[h] = has ? ex2(m - most) : 0.0f;
-        float all = has ? wt[h] * p[ROWS * C::LD + ROWS + r0 + h] : 0.0f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-        if (lane / LPR == h) {
-          top = most;
-          sum = all;
+      for (int w = 0; w <= NW; ++w) {
+        const bool has = w < NW ? (parts >> w) & 1u : start >= 0;
+        const float* p = w < NW ? rest + w * (C::PIECE / 4) : first;
+        x[w] = make_float4(0, 0, 0, 0);
+        ml[w] = make_float2(kLeast, 0.0f);
+        if (has) {
+          ml[w] = *reinterpret_cast<const float2*>(p + ROWS * C::LD + 2 * r);
+          x[w] = *reinterpret_cast<const float4*>(p + r * C::LD + d);
         }
       }
+      float top = kLeast, sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w <= NW; ++w) top = fmaxf(top, ml[w].x);
       float4 v = make_float4(0, 0, 0, 0);
-      auto add = [&](const float* p, int from) {
-        float f = __shfl_sync(0xFFFFFFFFu, wt[0], from);
 #pragma unroll
-        for (int h = 1; h < RPW; ++h) {
-          const float other = __shfl_sync(0xFFFFFFFFu, wt[h], from);
-          f = lane / LPR == h ? other : f;
-        }
-        const float4 x = *reinterpret_cast<const float4*>(p + r * C::LD + d);
-        v.x = fmaf(f, x.x, v.x);
-        v.y = fmaf(f, x.y, v.y);
-        v.z = fmaf(f, x.z, v.z);
-        v.w = fmaf(f, x.w, v.w);
-      };
-      if (start >= 0) add(first, 31);
-#pragma unroll
-      for (int w = 0; w < NW; ++w)
-        if ((parts >> w) & 1u) add(rest + w * (C::PIECE / 4), w);
+      for (int i = 0; i <= NW; ++i) {
+        const int w = i == 0 ? NW : i - 1;  // in the order of the units
+        const float f = ex2(ml[w].x - top);
+        sum = fmaf(f, ml[w].y, sum);
+        v.x = fmaf(f, x[w].x, v.x);
+        v.y = fmaf(f, x[w].y, v.y);
+        v.z = fmaf(f, x[w].z, v.z);
+        v.w = fmaf(f, x[w].w, v.w);
+      }
       if (whole) {
         const int row = item.x * ROWS + r, tok = quot(row, a.by_g);
         if (tok < item.w) {
