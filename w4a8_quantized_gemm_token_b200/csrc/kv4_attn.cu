@@ -916,35 +916,47 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
 
   // ---- join the pieces that meet in this block: a chain is a last piece (in its
   // warp's ring), if it began here, and the first pieces of the warps behind it
+  // (A chain is found by its bits, and a warp takes whole rows of it: what one warp does
+  // alone here costs four cycles an instruction at least.)
   const int my_flags = seg_flags[lane];
   const uint32_t heads = __ballot_sync(0xFFFFFFFFu, my_flags & 1);
-  const uint32_t end_at = __ballot_sync(0xFFFFFFFFu, my_flags & 2);
+  const uint32_t ends = __ballot_sync(0xFFFFFFFFu, my_flags & 2);
   const uint32_t tails = __ballot_sync(0xFFFFFFFFu, my_flags & 4);
+  const float* rest = reinterpret_cast<const float*>(smem + C::SM_HEAD);
+  constexpr int LPR = D / 4, RPW = 32 / LPR, TURNS = ROWS / RPW;  // lanes per row, rows per warp
   Meta meta = {};
-  // One row of a chain to a warp (D = 64: to half of one), all pieces' loads at once.
-  constexpr int LPR = D / 4, RPW = 32 / LPR;
-  int next = 0;  // the warp whose turn it is
-  auto emit = [&](int start, uint32_t parts, bool ended) {
-    const bool whole = start >= 0 && ended;
-    float* part = piece_at(a.ws, D, blk, start >= 0 ? 1 : 0);
+  int first_warp = 0;  // of the chain's first rows
+  // the chain's last piece, -1 where it began in an earlier block; the warps behind it
+  int start = -1;
+  uint32_t behind = 0xFFFFFFFFu;
+  if (heads == 0 || (tails & ((heads & (0u - heads)) - 1u)) != 0) {
+    start = tails != 0 ? __ffs(tails) - 1 : 32;
+    behind = tails != 0 ? 0xFFFFFFFEu << start : 0u;
+  }
+#pragma unroll 1
+  while (start < 32) {
+    const uint32_t end = ends & behind & (0u - (ends & behind));  // the warp that ends it, or none
+    const uint32_t parts = heads & behind & (end != 0 ? 2u * end - 1u : 0xFFFFFFFFu);
+    const bool whole = start >= 0 && end != 0;
     int4 item = make_int4(0, 0, 0, 0);
-    if (start >= 0) item = *reinterpret_cast<const int4*>(seg_item[start]);
-    if (!whole) {
-      meta.flags |= start >= 0 ? 4 : ended ? 3 : 1;
-      if (start >= 0) {
+    if (start >= 0) {
+      item = *reinterpret_cast<const int4*>(seg_item[start]);
+      if (!whole) {
+        meta.flags |= 4;
         meta.rt = item.x;
         meta.kvh = item.y;
         meta.row0 = item.z;
         meta.n = item.w;
       }
+    } else {
+      meta.flags |= end != 0 ? 3 : 1;
     }
     const float* first = reinterpret_cast<const float*>(smem + C::SM_RING + max(start, 0) * C::RING);
-    const float* rest = reinterpret_cast<const float*>(smem + C::SM_HEAD);
-    for (int r0 = 0; r0 < ROWS; r0 += RPW) {
-      const bool mine = next == warp;
-      next = next == NW - 1 ? 0 : next + 1;
-      if (!mine) continue;
-      const int r = r0 + lane / LPR, d = 4 * (lane % LPR);
+    int turn = warp - first_warp;
+    if (turn < 0) turn += NW;
+#pragma unroll 1
+    for (; turn < TURNS; turn += NW) {
+      const int r = turn * RPW + lane / LPR, d = 4 * (lane % LPR);
       float4 x[NW + 1];
       float2 ml[NW + 1];
 #pragma unroll
@@ -975,53 +987,35 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
       if (whole) {
         const int row = item.x * ROWS + r, tok = quot(row, a.by_g);
         if (tok < item.w) {
-          const float inv = sum > 0.0f ? 1.0f / sum : sum;
+          const float inv = sum > 0.0f ? __frcp_rn(sum) : sum;
           uint16_t* dst = a.out + ((long long)(item.z + tok) * a.H + item.y * a.G + row - tok * a.G) * D + d;
           *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
         }
       } else {
+        float* part = piece_at(a.ws, D, blk, start >= 0 ? 1 : 0);
         *reinterpret_cast<float4*>(part + r * D + d) = v;
-        if (d == 0) {
-          part[16 * D + r] = top;
-          part[16 * D + 16 + r] = sum;
-        }
+        if (d == 0) *reinterpret_cast<float2*>(part + 16 * D + 2 * r) = make_float2(top, sum);
       }
     }
-  };
-  int start = -1;       // the chain's last piece; -1: it began in an earlier block
-  uint32_t parts = 0;   // its first pieces
-  bool open = heads != 0 && (tails & ((heads & (0u - heads)) - 1u)) == 0;
-#pragma unroll 1
-  for (int w = 0; w <= NW; ++w) {
-    const uint32_t bit = w < NW ? 1u << w : 0u;
-    parts |= heads & bit;
-    const bool ended = (heads & end_at & bit) != 0;
-    if (open && (ended || w == NW)) emit(start, parts, ended);
-    if (ended) {
-      open = false;
-      parts = 0;
-    }
-    if (tails & bit) {
-      start = w;
-      parts = 0;
-      open = true;
-    }
+    first_warp = (first_warp + TURNS) % NW;
+    const uint32_t left = end != 0 ? tails & behind & ~(end - 1u) : 0u;
+    start = left != 0 ? __ffs(left) - 1 : 32;
+    behind = 0xFFFFFFFEu << (start & 31);
   }
   if (threadIdx.x == 0) reinterpret_cast<Meta*>(a.ws + kMetaOff)[blk] = meta;
 }
 
 // Joins the items that are cut between blocks: block (c, row) the one whose
 // beginning is block c's last piece, with the first pieces of the blocks behind it.
-// D / 4 threads read a piece's row; the 512 / D groups of them take the pieces in turn.
-// A launch waits for two loads, one after the other: every block's Meta, and then
-// the pieces' rows with their maxima and sums.
+// D / 4 threads read a piece's row; the 512 / D groups of them take the pieces in turn,
+// and then each other's sums.  A launch waits for two loads, one after the other:
+// every block's Meta, and then the pieces' rows with their maxima and sums.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(128) kv4_join_kernel(const Args a) {
   constexpr int TPP = D / 4, GROUPS = 128 / TPP, AHEAD = 4;
   __shared__ int flags[kMaxBlocks];
-  __shared__ float weight[kMaxBlocks];
   __shared__ __align__(16) float red[GROUPS][D];
-  __shared__ float total;
+  __shared__ __align__(8) float2 red_ml[GROUPS];
   pdl_launch_dependents();
   pdl_wait();
   const int c = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31;
@@ -1043,68 +1037,63 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Args a) {
     }
   }
   const int n = last - c + 1;
-  auto piece = [&](int i) { return piece_at(a.ws, D, c + i, i == 0 ? 1 : 0); };
-  auto has = [&](int i) { return i < n && (i == 0 || (flags[c + i] & 1) != 0); };
   const int grp = threadIdx.x / TPP, d = 4 * (threadIdx.x % TPP);
-  float4 x[AHEAD];
-#pragma unroll
-  for (int j = 0; j < AHEAD; ++j) {
-    const int i = grp + j * GROUPS;
-    x[j] = make_float4(0, 0, 0, 0);
-    if (has(i)) x[j] = *reinterpret_cast<const float4*>(piece(i) + r * D + d);
-  }
-  if (threadIdx.x < 32) {
-    constexpr int PER = (kMaxBlocks + 31) / 32;
-    float m[PER], l[PER], top = kLeast, sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int i = lane + 32 * j;
-      m[j] = has(i) ? piece(i)[16 * D + r] : kLeast;
-      l[j] = has(i) ? piece(i)[16 * D + 16 + r] : 0.0f;
-      top = fmaxf(top, m[j]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int i = lane + 32 * j;
-      const float f = has(i) ? ex2(m[j] - top) : 0.0f;
-      if (i < n) weight[i] = f;
-      if (f != 0.0f) sum = fmaf(f, l[j], sum);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) total = sum;
-  }
-  __syncthreads();
+  float top = kLeast, sum = 0.0f;
   float4 v = make_float4(0, 0, 0, 0);
-  auto add = [&](int i, const float4& y) {
-    const float f = i < n ? weight[i] : 0.0f;
-    if (f == 0.0f) return;
-    v.x = fmaf(f, y.x, v.x);
-    v.y = fmaf(f, y.y, v.y);
-    v.z = fmaf(f, y.z, v.z);
-    v.w = fmaf(f, y.w, v.w);
-  };
+#pragma unroll 1
+  for (int i0 = grp; i0 < n; i0 += AHEAD * GROUPS) {
+    float4 x[AHEAD];
+    float2 ml[AHEAD];
 #pragma unroll
-  for (int j = 0; j < AHEAD; ++j) add(grp + j * GROUPS, x[j]);
-#pragma unroll 4
-  for (int i = grp + AHEAD * GROUPS; i < n; i += GROUPS)
-    if (has(i)) add(i, *reinterpret_cast<const float4*>(piece(i) + r * D + d));
+    for (int j = 0; j < AHEAD; ++j) {
+      const int i = i0 + j * GROUPS;
+      x[j] = make_float4(0, 0, 0, 0);
+      ml[j] = make_float2(kLeast, 0.0f);
+      if (i < n && (i == 0 || (flags[c + i] & 1) != 0)) {
+        const float* p = piece_at(a.ws, D, c + i, i == 0 ? 1 : 0);
+        x[j] = *reinterpret_cast<const float4*>(p + r * D + d);
+        ml[j] = *reinterpret_cast<const float2*>(p + 16 * D + 2 * r);
+      }
+    }
+    float most = top;
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) most = fmaxf(most, ml[j].x);
+    const float keep = ex2(top - most);
+    top = most;
+    sum *= keep;
+    v = make_float4(v.x * keep, v.y * keep, v.z * keep, v.w * keep);
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const float f = ex2(ml[j].x - top);
+      sum = fmaf(f, ml[j].y, sum);
+      v.x = fmaf(f, x[j].x, v.x);
+      v.y = fmaf(f, x[j].y, v.y);
+      v.z = fmaf(f, x[j].z, v.z);
+      v.w = fmaf(f, x[j].w, v.w);
+    }
+  }
   *reinterpret_cast<float4*>(&red[grp][d]) = v;
+  if (d == 0) red_ml[grp] = make_float2(top, sum);
   __syncthreads();
   if (threadIdx.x >= TPP) return;
-#pragma unroll
-  for (int i = 1; i < GROUPS; ++i) {
-    const float4 y = *reinterpret_cast<const float4*>(&red[i][d]);
-    v.x += y.x;
-    v.y += y.y;
-    v.z += y.z;
-    v.w += y.w;
-  }
   const int row = me.rt * ROWS + r, tok = quot(row, a.by_g);
   if (tok >= me.n) return;
-  const float sum = total, inv = sum > 0.0f ? 1.0f / sum : sum;
+  float most = kLeast;
+#pragma unroll
+  for (int i = 0; i < GROUPS; ++i) most = fmaxf(most, red_ml[i].x);
+  v = make_float4(0, 0, 0, 0);
+  sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < GROUPS; ++i) {
+    const float f = ex2(red_ml[i].x - most);
+    const float4 x = *reinterpret_cast<const float4*>(&red[i][d]);
+    sum = fmaf(f, red_ml[i].y, sum);
+    v.x = fmaf(f, x.x, v.x);
+    v.y = fmaf(f, x.y, v.y);
+    v.z = fmaf(f, x.z, v.z);
+    v.w = fmaf(f, x.w, v.w);
+  }
+  const float inv = sum > 0.0f ? __frcp_rn(sum) : sum;
   uint16_t* dst = a.out + ((long long)(me.row0 + tok) * a.H + me.kvh * a.G + row - tok * a.G) * D + d;
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
 }
