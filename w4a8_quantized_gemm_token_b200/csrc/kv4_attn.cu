@@ -938,6 +938,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
     const uint32_t end = ends & behind & (0u - (ends & behind));  // the warp that ends it, or none
     const uint32_t parts = heads & behind & (end != 0 ? 2u * end - 1u : 0xFFFFFFFFu);
     const bool whole = start >= 0 && end != 0;
+    // (the warps of a chain are next to each other)
+    const int pieces = __popc(parts) + (start >= 0), from = start >= 0 ? start : __ffs(parts) - 1;
     int4 item = make_int4(0, 0, 0, 0);
     if (start >= 0) {
       item = *reinterpret_cast<const int4*>(seg_item[start]);
@@ -957,32 +959,34 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
 #pragma unroll 1
     for (; turn < TURNS; turn += NW) {
       const int r = turn * RPW + lane / LPR, d = 4 * (lane % LPR);
-      float4 x[NW + 1];
-      float2 ml[NW + 1];
-#pragma unroll
-      for (int w = 0; w <= NW; ++w) {
-        const bool has = w < NW ? (parts >> w) & 1u : start >= 0;
-        const float* p = w < NW ? rest + w * (C::PIECE / 4) : first;
-        x[w] = make_float4(0, 0, 0, 0);
-        ml[w] = make_float2(kLeast, 0.0f);
-        if (has) {
-          ml[w] = *reinterpret_cast<const float2*>(p + ROWS * C::LD + 2 * r);
-          x[w] = *reinterpret_cast<const float4*>(p + r * C::LD + d);
-        }
-      }
       float top = kLeast, sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w <= NW; ++w) top = fmaxf(top, ml[w].x);
       float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 1
+      for (int q0 = 0; q0 < pieces; q0 += 4) {
+        float4 x[4];
+        float2 ml[4];
 #pragma unroll
-      for (int i = 0; i <= NW; ++i) {
-        const int w = i == 0 ? NW : i - 1;  // in the order of the units
-        const float f = ex2(ml[w].x - top);
-        sum = fmaf(f, ml[w].y, sum);
-        v.x = fmaf(f, x[w].x, v.x);
-        v.y = fmaf(f, x[w].y, v.y);
-        v.z = fmaf(f, x[w].z, v.z);
-        v.w = fmaf(f, x[w].w, v.w);
+        for (int j = 0; j < 4; ++j) {
+          const int q = min(q0 + j, pieces - 1);  // (behind the last one: it again, with weight 0)
+          const float* p = start >= 0 && q == 0 ? first : rest + (from + q) * (C::PIECE / 4);
+          ml[j] = *reinterpret_cast<const float2*>(p + ROWS * C::LD + 2 * r);
+          x[j] = *reinterpret_cast<const float4*>(p + r * C::LD + d);
+          if (q0 + j >= pieces) ml[j] = make_float2(-INFINITY, 0.0f);
+        }
+        const float most = fmaxf(fmaxf(top, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+        const float keep = ex2(top - most);
+        top = most;
+        sum *= keep;
+        v = make_float4(v.x * keep, v.y * keep, v.z * keep, v.w * keep);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float f = ex2(ml[j].x - top);
+          sum = fmaf(f, ml[j].y, sum);
+          v.x = fmaf(f, x[j].x, v.x);
+          v.y = fmaf(f, x[j].y, v.y);
+          v.z = fmaf(f, x[j].z, v.z);
+          v.w = fmaf(f, x[j].w, v.w);
+        }
       }
       if (whole) {
         const int row = item.x * ROWS + r, tok = quot(row, a.by_g);
