@@ -216,8 +216,12 @@ __device__ __forceinline__ uint32_t record_number(const Args& a, const Item& it,
   return ((uint32_t)id * (uint32_t)a.cache.Hkv + (uint32_t)it.kvh) * (uint32_t)a.by_page.d + (uint32_t)in;
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+template <int kBytes>
+__device__ __forceinline__ void copy(uint32_t dst, const uint8_t* src) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -263,18 +267,17 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 __device__ __forceinline__ int exponent(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
 
-template <int N>
-__device__ __forceinline__ void lds(uint32_t (&r)[N], const uint8_t* p) {
+// 4 N bytes at a shared address; kOff: more bytes.
+template <int kOff, int N>
+__device__ __forceinline__ void lds(uint32_t (&r)[N], uint32_t at) {
   static_assert(N == 1 || N == 2 || N == 4, "4, 8 or 16 bytes");
-  if constexpr (N == 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
-  } else if constexpr (N == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    r[0] = v.x; r[1] = v.y;
-  } else {
-    r[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4+%5];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at), "n"(kOff));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2+%3];" : "=r"(r[0]), "=r"(r[1]) : "r"(at), "n"(kOff));
+  else
+    asm volatile("ld.shared.u32 %0, [%1+%2];" : "=r"(r[0]) : "r"(at), "n"(kOff));
 }
 
 // The largest finite scale of a key's groups.
@@ -481,16 +484,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
     const int g = lane >> 2, t = lane & 3;
     const uint8_t* ring = smem + C::SM_RING + warp * C::RING;
     // this lane's places in a record: codes of tokens g, g + 8; of pairs t, t + 4
-    const uint8_t* ring_k = ring + (g * 4 + t) * 8 * NG;
-    const uint8_t* ring_v = ring + L::V_OFF + (t * 8 + g) * 8 * NG;
-    const uint8_t* ring_s = ring + L::KS_OFF + g * 4 * NG;
+    const uint32_t ring_k = smem_u32(ring) + (g * 4 + t) * 8 * NG;
+    const uint32_t ring_v = smem_u32(ring) + L::V_OFF + (t * 8 + g) * 8 * NG;
+    const uint32_t ring_s = smem_u32(ring) + L::KS_OFF + g * 4 * NG;
     bool first_piece = k > 0;
     int flags = 0;
     int done = 0;   // units worked on
     int asked = 0;  // units whose copies are issued, or passed over
     int known = 0;  // units that are numbered
-    const uint8_t* cache = a.cache.base + 16 * lane;
     const uint32_t ring_dst = smem_u32(ring) + 16 * lane;
+    uint32_t missing = 0, missing_next = 0;  // units of `done`'s window, and of the next, with no record
     // Numbers the next window of units, a lane each; the units of one item look their
     // pages up together.
     auto number_more = [&]() {
@@ -518,26 +521,28 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
           next_item<ROWS>(a, at);
         }
       }
-      number[(known + lane) % (2 * WINDOW)] = mine;
+      const uint32_t none = __ballot_sync(0xFFFFFFFFu, mine == kNoRecord);
+      (known == 0 ? missing : missing_next) = none;
+      // (a record that is not there: the first one is copied in its place, and masked)
+      number[(known + lane) % (2 * WINDOW)] = mine == kNoRecord ? 0u : mine;
       known += want;
       __syncwarp();
       if (lane == 0) *reinterpret_cast<int4*>(ahead[warp]) = make_int4(at.b, at.rt, at.kvh, u);
     };
     // A unit's copies into its place in the ring.
-    auto copy = [&](int unit, uint32_t place) {
-      const uint32_t rec = number[unit % (2 * WINDOW)];
-      const uint8_t* src = cache + (unsigned long long)rec * L::REC;
-      const uint32_t dst = ring_dst + place;
-      if (rec != kNoRecord) {
+    auto fetch = [&](int unit, uint32_t place) {
+      uint32_t rec[1];
+      lds<0>(rec, smem_u32(number) + unit % (2 * WINDOW) * 4);
+      const uint8_t* src = a.cache.base + (unsigned long long)rec[0] * L::REC;
 #pragma unroll
-        for (int i = 0; i < L::REC / 512; ++i) copy16(dst + 512 * i, src + 512 * i);
-        if (lane < L::REC % 512 / 16) copy16(dst + L::REC / 512 * 512, src + L::REC / 512 * 512);
-      }
+      for (int i = 0; i < L::KS_OFF / 512; ++i) copy<16>(ring_dst + place + 512 * i, src + 16 * lane + 512 * i);
+      constexpr int kScales = (L::REC - L::KS_OFF) / 32;  // 8 or 4 bytes a lane
+      copy<kScales>(ring_dst + place + L::KS_OFF - (16 - kScales) * lane, src + kScales * lane + L::KS_OFF);
     };
     if (units > 0) number_more();
 #pragma unroll 1
     for (; asked < STAGES; ++asked) {
-      if (asked < units) copy(asked, asked * L::REC);
+      if (asked < units) fetch(asked, asked * L::REC);
       copies_commit();
     }
     uint32_t place = 0;  // of unit `done` in the ring, and then of unit `asked`
@@ -546,15 +551,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
       // queries: fragments of row g (per j and half of a word's nibbles, the second
       // of a pair a 16th); sums and factors of rows 2 t, 2 t + 1, the columns of the scores
       uint32_t qb[NT][NG][2][4];
-      float qs[NT][2][NG], R[NT][2];
+      uint32_t qo[NT];  // sum(q) per group in three fp16 pieces, a lane of the row to a piece
+      float R[NT][2];
       int pos[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float top = 0.0f, sum[NG];
 #pragma unroll
-        for (int grp = 0; grp < NG; ++grp) {
-          sum[grp] = 0.0f;
-        }
+        for (int grp = 0; grp < NG; ++grp) sum[grp] = 0.0f;
 #pragma unroll
         for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
@@ -584,6 +588,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
           sum[grp] += __shfl_xor_sync(0xFFFFFFFFu, sum[grp], 1);
           sum[grp] += __shfl_xor_sync(0xFFFFFFFFu, sum[grp], 2);
         }
+        // (up to 2^20 in the queries' unit: 2^-7 brings it into fp16's range)
+        float piece[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) {
+          float rest = sum[grp] * f * 0x1p-7f;
+          const float first = __half2float(__float2half_rn(rest));
+          rest = t == 0 ? first : rest - first;
+          const float second = __half2float(__float2half_rn(rest));
+          rest = t <= 1 ? second : rest - second;
+          piece[grp] = t == 3 ? 0.0f : rest;
+        }
+        qo[n] = pack_f16(piece[0], piece[1]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int from = 4 * (2 * t + c);  // a lane of row 2 t + c
@@ -591,9 +607,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
           // the scores' unit: x = 2^(24 + e) times what the codes' product gives
           // (neither 0 nor infinite: a masked score is -inf, one of 0 stays 0)
           R[n][c] = fminf(fmaxf(a.sc * pow2(min(24 + ec, 127)), 1.0e-35f), 3.0e38f);
-#pragma unroll
-          for (int grp = 0; grp < NG; ++grp)
-            qs[n][c][grp] = __shfl_sync(0xFFFFFFFFu, sum[grp], from) * (pow2(-ec) * 0x1p-24f);
           const int rc = it.rt * ROWS + 8 * n + 2 * t + c;
           const int tc = quot(rc, a.by_g);
           pos[n][c] = tc < it.n ? it.len - it.n + tc : -1;
@@ -639,17 +652,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
         constexpr bool kMask = decltype(masks)::value;
         copies_wait<STAGES - 1>();
         __syncwarp();
-        const uint8_t* at_k = ring_k + place;
-        const uint8_t* at_v = ring_v + place;
-        const uint8_t* at_s = ring_s + place;
+        const uint32_t at_k = ring_k + place, at_v = ring_v + place, at_s = ring_s + place;
         // ---- scores: x[n][i], i = 0, 1 key g and rows 2 t, 2 t + 1; i = 2, 3 key g + 8
         float x[NT][4];
         {
           uint32_t k0[2 * NG], k1[2 * NG], s0[NG], s1[NG];
-          lds(k0, at_k);
-          lds(k1, at_k + 8 * 4 * 8 * NG);
-          lds(s0, at_s);
-          lds(s1, at_s + 8 * 4 * NG);
+          lds<0>(k0, at_k);
+          lds<8 * 4 * 8 * NG>(k1, at_k);
+          lds<0>(s0, at_s);
+          lds<8 * 4 * NG>(s1, at_s);
+          // the offsets' part, 2^17-fold: keys by groups, times groups by rows, a pair of
+          // columns to each piece of the sums
+          const uint32_t o0 = NG == 2 ? __byte_perm(s0[0], s0[NG - 1], 0x7632) : s0[0] >> 16;
+          const uint32_t o1 = NG == 2 ? __byte_perm(s1[0], s1[NG - 1], 0x7632) : s1[0] >> 16;
 #pragma unroll
           for (int grp = 0; grp < NG; ++grp) {
             float acc[NT][4];
@@ -670,15 +685,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
                 d >>= 8;
               }
             }
-            const float2 a0 = unpack_f16(s0[grp]), a1 = unpack_f16(s1[grp]);
+            const float a0 = unpack_f16(s0[grp]).x, a1 = unpack_f16(s1[grp]).x;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const float z0 = a0.y * qs[n][c][grp], z1 = a1.y * qs[n][c][grp];
-                x[n][c] = fmaf(a0.x, acc[n][c], grp == 0 ? z0 : x[n][c] + z0);
-                x[n][2 + c] = fmaf(a1.x, acc[n][2 + c], grp == 0 ? z1 : x[n][2 + c] + z1);
+                x[n][c] = grp == 0 ? a0 * acc[n][c] : fmaf(a0, acc[n][c], x[n][c]);
+                x[n][2 + c] = grp == 0 ? a1 * acc[n][2 + c] : fmaf(a1, acc[n][2 + c], x[n][2 + c]);
               }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma(acc, o0, o1, 0u, 0u, qo[n], 0u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[n][i] = fmaf(acc[i], 0x1p-17f, x[n][i]);
           }
         }
         if constexpr (kMask) {
@@ -695,22 +716,46 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
         }
         // ---- values and their scales; the record's place is free then
         uint32_t v0[2 * NG], v1[2 * NG], t0[NG], t1[NG];
-        lds(v0, at_v);
-        lds(v1, at_v + 4 * 8 * 8 * NG);
-        lds(t0, at_s + 16 * 4 * NG);
-        lds(t1, at_s + 24 * 4 * NG);
+        lds<0>(v0, at_v);
+        lds<4 * 8 * 8 * NG>(v1, at_v);
+        lds<16 * 4 * NG>(t0, at_s);
+        lds<24 * 4 * NG>(t1, at_s);
         __syncwarp();  // every lane has read the record
-        if (more) copy(asked, place);
+        if (more) fetch(asked, place);
         copies_commit();
         ++asked;
         place = place == (STAGES - 1) * L::REC ? 0 : place + L::REC;
-        // ---- a row's reference moves only where a score passes the last maximum by 2^4
-        bool turn = false;
+        // ---- weights, and times scales, as the second product's operand.  A row's reference
+        // moves where a score passes the last maximum by 2^4, or a product comes to 2^15 (the
+        // half then carries into its sign bit)
+        uint32_t w[NT][NG][2];
+        float y[NT][4];
+        auto weights = [&]() {
+          uint32_t big = 0;
+#pragma unroll
+          for (int grp = 0; grp < NG; ++grp) {
+            const float s0 = unpack_f16(t0[grp]).x, s1 = unpack_f16(t1[grp]).x;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              weigh<kMask>(y[n], s0, s1, w[n][grp]);
+              big = __vmaxu2(big, __vmaxu2(w[n][grp][0], w[n][grp][1]));
+            }
+          }
+          return ((big + 0x08000800u) & 0x80008000u) != 0;
+        };
+        auto exponentials = [&]() {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[n][i] = ex2(fmaf(x[n][i], R[n][i & 1], nm[n][i & 1]));
+        };
+        exponentials();
+        bool move = weights();
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) turn |= fmaxf(x[n][c], x[n][2 + c]) > lim[n][c];
-        if (__builtin_expect(__any_sync(0xFFFFFFFFu, turn), 0)) {
+          for (int c = 0; c < 2; ++c) move |= fmaxf(x[n][c], x[n][2 + c]) > lim[n][c];
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, move), 0)) {
           const float m0 = largest_scale(t0), m1 = largest_scale(t1);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
@@ -721,57 +766,24 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
               const float heavy = column_max(fmaxf(ex2((x[n][c] - top) * R[n][c]) * m0,
                                                    ex2((x[n][2 + c] - top) * R[n][c]) * m1));
               const float was = nm[n][c];
+              const float set = (float)(9 - exponent(fmaxf(heavy, 0x1p-24f))) - fmaxf(top * R[n][c], kLeast);
               if (top > lim[n][c]) {
-                nm[n][c] = (float)(9 - exponent(fmaxf(heavy, 0x1p-24f))) - fmaxf(top * R[n][c], kLeast);
+                nm[n][c] = set;
                 lim[n][c] = top + 4.0f / R[n][c];
+              } else if (top > -INFINITY && set < nm[n][c] - 4.0f) {
+                nm[n][c] = set;  // products of 2^13 and more
               }
               alpha[c] = ex2(nm[n][c] - was);
             }
             rescale(n, alpha);
           }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[n][i] = ex2(fmaf(x[n][i], R[n][i & 1], nm[n][i & 1]));
-        // ---- weights times scales, as the second product's operand
-        uint32_t w[NT][NG][2];
-        auto weights = [&]() {
-          uint32_t big = 0;
-#pragma unroll
-          for (int grp = 0; grp < NG; ++grp) {
-            const float s0 = unpack_f16(t0[grp]).x, s1 = unpack_f16(t1[grp]).x;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              weigh<kMask>(x[n], s0, s1, w[n][grp]);
-              big = __vmaxu2(big, __vmaxu2(w[n][grp][0], w[n][grp][1]));
-            }
-          }
-          return big;
-        };
-        // a half of 2^15 or more carries into its sign bit
-        if (__builtin_expect(__any_sync(0xFFFFFFFFu, ((weights() + 0x08000800u) & 0x80008000u) != 0), 0)) {
-          const float m0 = largest_scale(t0), m1 = largest_scale(t1);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float alpha[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const float heavy = column_max(fmaxf(x[n][c] * m0, x[n][2 + c] * m1));
-              const float was = nm[n][c];
-              if (heavy >= 0x1p14f) nm[n][c] -= (float)(exponent(heavy) - 9);
-              alpha[c] = ex2(nm[n][c] - was);
-              x[n][c] *= alpha[c];
-              x[n][2 + c] *= alpha[c];
-            }
-            rescale(n, alpha);
-          }
+          exponentials();
           weights();
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          l[n][0] += x[n][0] + x[n][2];
-          l[n][1] += x[n][1] + x[n][3];
+          l[n][0] += y[n][0] + y[n][2];
+          l[n][1] += y[n][1] + y[n][3];
         }
 #pragma unroll
         for (int grp = 0; grp < NG; ++grp) {
@@ -780,7 +792,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float y0 = x[n][c], y1 = x[n][2 + c];
+              const float y0 = y[n][c], y1 = y[n][2 + c];
               if (kMask)
                 off[n][c][grp] += (y0 == 0.0f ? 0.0f : y0 * o0) + (y1 == 0.0f ? 0.0f : y1 * o1);
               else
@@ -819,10 +831,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
         const bool whole = k >= it.whole0 && k < it.whole1;
         if (whole) n = min(n, it.whole1 - k);
         if (k < it.whole0) n = min(n, it.whole0 - k);
-        const uint32_t missing = __ballot_sync(0xFFFFFFFFu, number[(done / WINDOW * WINDOW + lane) % (2 * WINDOW)] == kNoRecord) >>
-                                 (done % WINDOW);
-        const bool dead = missing & 1u;
-        if (missing != 0) n = dead ? 1 : min(n, __ffs(missing) - 1);
+        const uint32_t none = missing >> (done % WINDOW);
+        const bool dead = none & 1u;
+        if (none != 0) n = dead ? 1 : min(n, __ffs(none) - 1);
         const int end = k + n;
         if (whole && !dead) {
 #pragma unroll 1
@@ -832,6 +843,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
           for (; k < end; ++k) step(std::true_type{}, record_of(it, k), dead, more);
         }
         done += n;
+        if (done % WINDOW == 0) missing = missing_next;
       }
       // ---- the segment's sums: l and the offsets' part over the lanes of a row; then
       // z = O of row 2 t + c, dims 64 group + 8 g + 4 h + 2 i + (0, 1)
