@@ -216,12 +216,14 @@ __device__ __forceinline__ uint32_t record_number(const Args& a, const Item& it,
   return ((uint32_t)id * (uint32_t)a.cache.Hkv + (uint32_t)it.kvh) * (uint32_t)a.by_page.d + (uint32_t)in;
 }
 
-template <int kBytes>
+// kBytes (16, or 8 or 4), kAt bytes behind both addresses.
+template <int kBytes, int kAt>
 __device__ __forceinline__ void copy(uint32_t dst, const uint8_t* src) {
   if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%2], 16;" ::"r"(dst), "l"(src), "n"(kAt) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0+%2], [%1+%2], %3;" ::"r"(dst), "l"(src), "n"(kAt), "n"(kBytes)
+                 : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -533,11 +535,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
     auto fetch = [&](int unit, uint32_t place) {
       uint32_t rec[1];
       lds<0>(rec, smem_u32(number) + unit % (2 * WINDOW) * 4);
-      const uint8_t* src = a.cache.base + (unsigned long long)rec[0] * L::REC;
-#pragma unroll
-      for (int i = 0; i < L::KS_OFF / 512; ++i) copy<16>(ring_dst + place + 512 * i, src + 16 * lane + 512 * i);
-      constexpr int kScales = (L::REC - L::KS_OFF) / 32;  // 8 or 4 bytes a lane
-      copy<kScales>(ring_dst + place + L::KS_OFF - (16 - kScales) * lane, src + kScales * lane + L::KS_OFF);
+      const uint8_t* src = a.cache.base + (unsigned long long)rec[0] * L::REC + 16 * lane;
+      const uint32_t dst = ring_dst + place;
+      copy<16, 0>(dst, src);
+      copy<16, 512>(dst, src);
+      if constexpr (NG == 2) {
+        copy<16, 1024>(dst, src);
+        copy<16, 1536>(dst, src);
+      }
+      static_assert(L::KS_OFF == 1024 * NG && L::REC - L::KS_OFF == 32 * 4 * NG, "the copies");
+      copy<4 * NG, L::KS_OFF>(dst - (16 - 4 * NG) * lane, src - (16 - 4 * NG) * lane);
     };
     if (units > 0) number_more();
 #pragma unroll 1
