@@ -569,8 +569,8 @@ qk_status qk_rope(const uint16_t *q, int64_t q_stride, uint16_t *q_out, int64_t 
  * a negative position) records QK_ERR_INDEX for qk_check_device_error and skips
  * that token: nothing outside the buffers is read or written.
  * Shape contract: D = 64 or 128; page % 16 == 0, 16 <= page <= 1024;
- * Hkv >= 1; 1 <= num_pages, max_pages; max_pages page <= 2^30; T <= 2^30; B >= 1
- * (T = 0 is a no-op).  16-byte alignment; row strides (in elements) >= heads D
+ * Hkv >= 1; 1 <= num_pages, max_pages; num_pages Hkv page / 16 < 2^32 - 1 (records);
+ * max_pages page <= 2^30; T <= 2^30; B >= 1 (T = 0 is a no-op).  16-byte alignment; row strides (in elements) >= heads D
  * and multiples of 8.
  */
 
@@ -612,7 +612,7 @@ size_t qk_kv4_attention_workspace_size(int64_t D);
  * fp32, the softmax and its sums are fp32, a weight times its value's scale enters
  * the second product as fp16 (11 bits), and out is rounded once to bf16: the
  * error is that rounding plus at most about 2^-11 sum_j P_j 15 scale_j (and the
- * scores' fp32 sums).  Deterministic; a request's result does not depend on the rest
+ * fp32 sums').  Deterministic; a request's result does not depend on the rest
  * of the batch beyond the order in which its parts are joined.
  *   q         : bf16 bits, row t at q + t q_stride, H heads of D (in)
  *   scale     : finite, >= 0;  window, sinks: >= 0 (window = 0: all keys),
@@ -624,8 +624,8 @@ size_t qk_kv4_attention_workspace_size(int64_t D);
  *               workspaces of their own.  Nothing in it is kept.
  * Pages in front of every row's window (and behind the sinks) are not read and
  * may be freed.  (H / Hkv) T <= 2^30.
- * Kernels: the attention (one block per SM, equal spans of the cache) and the
- * join of what was cut between blocks.
+ * Kernels: the attention (one block per SM, a warp per equal span of the cache)
+ * and the join of what was cut between blocks.
  */
 qk_status qk_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t T, int64_t H, int64_t Hkv,
                            int64_t D, const void *cache, int64_t num_pages, int64_t page,

@@ -132,6 +132,9 @@ def test_kv4_sizes(qk):
         assert qk.qk_kv4_cache_size(*bad) == 0
     assert qk.qk_kv4_attention_workspace_size(128) > qk.qk_kv4_attention_workspace_size(64) > 0
     assert qk.qk_kv4_attention_workspace_size(96) == 0
+    # records have 32-bit numbers
+    assert qk.qk_kv4_cache_size((1 << 26) - 1, 64, 16, 64) == ((1 << 26) - 1) * 64 * 16 * 72
+    assert qk.qk_kv4_cache_size(1 << 26, 64, 16, 64) == 0
 
 
 @pytest.mark.parametrize("D", [64, 128])

@@ -190,6 +190,10 @@ def test_few_rows_and_windows(qk, D, G, page, window, sinks):  # noqa: F811
     ([100] * 300, [1] * 300, 2, 2, 64),   # more requests than threads / 2
     ([40] * 700, [2] * 700, 1, 1, 128),   # more requests than threads
     ([777] * 40, [1] * 40, 8, 5, 128),
+    ([40] * 600, [16] * 600, 1, 1, 128),  # two tiles of rows, several requests to a thread
+    ([50] * 800, [12] * 800, 1, 2, 64),
+    ([16] * 500, [1] * 500, 4, 8, 64),    # items of one record, many to a warp
+    ([3000] + [0, 1, 17] * 60, [1] + [0, 1, 1] * 60, 2, 8, 128),
 ])
 def test_spans(qk, lens, rows, Hkv, G, D):  # noqa: F811
     """Items cut within warps, blocks and between blocks; the same bits on a second run."""
@@ -418,6 +422,29 @@ def test_bad_pages_and_lengths(qk):  # noqa: F811
     with pytest.raises(qk.QKError):
         qk.qk_check_device_error()
     qk.qk_check_device_error()
+
+
+@pytest.mark.parametrize("D,G", [(128, 4), (64, 16)])
+def test_missing_pages_of_a_long_request(qk, D, G):  # noqa: F811
+    """Pages that are not there, first, last, next to each other and alone: their keys are as if
+    masked, whatever the first page of the cache holds."""
+    n, page = 9000, 16
+    c = Batch(qk, [n, 40], [1, 1], 1, D, page, seed=D)
+    q = c.q(G)
+    gone = sorted({0, 1, 31, 32, 33, 100, 200, 201, 202, 203, 204, 205, 400, (n - 1) // page})
+    table = c.table.clone()
+    table[0, gone] = i32([-1, c.P] * (len(gone) // 2))
+    out = qk.qk_kv4_attention(q, c.cache, table, c.lens, c.cu)
+    with pytest.raises(qk.QKError) as e:
+        qk.qk_check_device_error()
+    assert e.value.status == INDEX
+    k, v = ref.request_kv(c.cache, c.table[0], n, D)
+    keep = torch.ones(n, dtype=torch.bool, device="cuda")
+    for g in gone:
+        keep[page * g:page * g + page] = False
+    want, tol = ref.attention(q[:1], k[keep], v[keep], D ** -0.5, 0, 0)
+    assert ((out[:1].double() - want).abs() <= tol).all()
+    c.check(q, out, requests=[1])
 
 
 def test_freed_pages_behind_the_window(qk):  # noqa: F811
