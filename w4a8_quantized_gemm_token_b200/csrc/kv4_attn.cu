@@ -477,8 +477,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
       load_tile<ROWS>(a, it);
       it.kvh = rest >> 31 ? (int)(rest / it.cnt) : (int)((uint32_t)rest / (uint32_t)it.cnt);
       k = (int)(rest - (long long)it.kvh * it.cnt);
+      // (the ids of the first pages are on their way while the queries' addresses are made)
+      if (it.p1 >= 0 && k + lane < it.cnt)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(a.req.page_table + (long long)it.b * a.req.max_pages +
+                                                     page_of(a, it, k + lane)));
       load_queries();
-      if (lane == 0) *reinterpret_cast<int4*>(ahead[warp]) = make_int4(it.b, it.rt, it.kvh, k);
     }
   }
 
@@ -496,21 +499,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
     int known = 0;  // units that are numbered
     const uint32_t ring_dst = smem_u32(ring) + 16 * lane;
     uint32_t missing = 0, missing_next = 0;  // units of `done`'s window, and of the next, with no record
-    // Numbers the next window of units, a lane each; the units of one item look their
-    // pages up together.
-    auto number_more = [&]() {
-      __syncwarp();
-      const int4 from = *reinterpret_cast<const int4*>(ahead[warp]);
-      Item at;
-      at.b = from.x;
-      at.rt = from.y;
-      at.kvh = from.z;
-      int u = from.w, have = 0;
-      if (per == 1)
-        set_request<ROWS>(a, at, seqs[at.b]);
-      else
-        load_request<ROWS>(a, at);
-      load_tile<ROWS>(a, at);
+    // Numbers the next window of units, from unit u of an item on, a lane each; the units
+    // of one item look their pages up together.
+    auto number_from = [&](Item at, int u) {
+      int have = 0;
       const int want = min(WINDOW, units - known);
       uint32_t mine = kNoRecord;
       while (have < want) {
@@ -530,6 +522,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
       known += want;
       __syncwarp();
       if (lane == 0) *reinterpret_cast<int4*>(ahead[warp]) = make_int4(at.b, at.rt, at.kvh, u);
+      __syncwarp();
+    };
+    auto number_more = [&]() {
+      const int4 from = *reinterpret_cast<const int4*>(ahead[warp]);
+      Item at;
+      at.b = from.x;
+      at.rt = from.y;
+      at.kvh = from.z;
+      if (per == 1)
+        set_request<ROWS>(a, at, seqs[at.b]);
+      else
+        load_request<ROWS>(a, at);
+      load_tile<ROWS>(a, at);
+      number_from(at, from.w);
     };
     // A unit's copies into its place in the ring.
     auto fetch = [&](int unit, uint32_t place) {
@@ -546,7 +552,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
       static_assert(L::KS_OFF == 1024 * NG && L::REC - L::KS_OFF == 32 * 4 * NG, "the copies");
       copy<4 * NG, L::KS_OFF>(dst - (16 - 4 * NG) * lane, src - (16 - 4 * NG) * lane);
     };
-    if (units > 0) number_more();
+    if (units > 0) number_from(it, k);
 #pragma unroll 1
     for (; asked < STAGES; ++asked) {
       if (asked < units) fetch(asked, asked * L::REC);
