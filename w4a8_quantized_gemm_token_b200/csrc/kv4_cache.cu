@@ -147,18 +147,18 @@ __global__ void __launch_bounds__(kThreads)
   // step q: row first + q % n, head group q / n
   auto load = [&](int r, int h0) {
     const long long row = first + r;
-    const uint16_t* src = me.is_v ? v + row * v_stride : k + row * k_stride;
+    const uint4* src = reinterpret_cast<const uint4*>((me.is_v ? v + row * v_stride : k + row * k_stride) +
+                                                      (h0 + me.sub) * D) + me.d8;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-      const int head = h0 + i * me.STEP + me.sub;
       next[i] = make_uint4(0, 0, 0, 0);
-      if (head < cache.Hkv) next[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)head * D) + me.d8);
+      if (h0 + i * me.STEP + me.sub < cache.Hkv) next[i] = __ldg(src + i * me.STEP * (D / 8));
     }
   };
   int r = 0, h0 = blockIdx.y * kHeads * me.STEP;
   load(r, h0);  // (every row < T is there, whosever it is)
   const Place all = find_tokens(req, cache, by_page, first, n, L::REC, err);
-  const long long head_bytes = (long long)(cache.page >> 4) * L::REC;
+  const int head_bytes = (cache.page >> 4) * L::REC, step_bytes = me.STEP * head_bytes;  // (< 2^19)
   // of the eight lanes of a group, two hold step `mine`'s extremes after the exchange
   const int lane = threadIdx.x & 31, mine = (lane & 1) * 2 + ((lane >> 1) & 1);
   for (;;) {
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads)
       continue;
     }
     const int code = me.code(place), scale = me.scale(place);
-    uint8_t* rec = cache.base + at + (head0 + me.sub) * head_bytes;
+    uint8_t* rec = cache.base + at + (long long)(head0 + me.sub) * head_bytes;
     uint32_t m[kHeads];  // (max, -min) of the step's group: over the lane, then over the group
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
@@ -199,9 +199,10 @@ __global__ void __launch_bounds__(kThreads)
     // (a scale of 0 has only codes 0)
     const float inv = __low2float(so) != 0.0f ? 0.0625f * __frcp_rn(__low2float(so)) : 0.0f;
     if (!(lane & 4) && head0 + mine * me.STEP + me.sub < cache.Hkv)
-      *reinterpret_cast<__half2*>(rec + mine * me.STEP * head_bytes + scale) = so;
+      *reinterpret_cast<__half2*>(rec + mine * step_bytes + scale) = so;
+    uint8_t* dst = rec + code;
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
+    for (int i = 0; i < kHeads; ++i, dst += step_bytes) {
       const int from_lane = (lane & 24) + (i >> 1) + (i & 1) * 2;  // step i's
       const float off = __half2float(__ushort_as_half(
           (unsigned short)__shfl_sync(0xFFFFFFFFu, (int)__half_as_ushort(__high2half(so)), from_lane)));
@@ -221,7 +222,6 @@ __global__ void __launch_bounds__(kThreads)
       }
       packed -= kBits * 0x11111111u;
       if (head0 + i * me.STEP + me.sub >= cache.Hkv) continue;
-      uint8_t* dst = rec + i * me.STEP * head_bytes + code;
       if (!me.is_v) {
         *reinterpret_cast<uint32_t*>(dst) = packed;
       } else {
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads)
   const int first = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * run;
   const int n = min(run, req.T - first);
   if (n <= 0) return;
-  const long long head_bytes = (long long)(cache.page >> 4) * L::REC;
+  const int head_bytes = (cache.page >> 4) * L::REC, step_bytes = me.STEP * head_bytes;  // (< 2^19)
   const int groups = gridDim.y * kHeads * me.STEP;
   const Place all = find_tokens(req, cache, by_page, first, n, L::REC, err);
   uint2 codes[kHeads];
@@ -261,14 +261,14 @@ __global__ void __launch_bounds__(kThreads)
   auto load = [&](int r, int h0) {
     const long long at = __shfl_sync(0xFFFFFFFFu, all.at, r);
     place = __shfl_sync(0xFFFFFFFFu, all.in, r);
-    const uint8_t* rec = cache.base + at + (h0 + me.sub) * head_bytes;
+    const uint8_t* rec = cache.base + at + (long long)(h0 + me.sub) * head_bytes;
     const int code = me.code(place) & ~3, scale = me.scale(place);  // (a V word holds two tokens)
+    const uint8_t* src = rec;
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
+    for (int i = 0; i < kHeads; ++i, src += step_bytes) {
       codes[i] = make_uint2(0, 0);
       so[i] = 0;
       if (place < 0 || h0 + i * me.STEP + me.sub >= cache.Hkv) continue;
-      const uint8_t* src = rec + i * me.STEP * head_bytes;
       if (me.is_v)
         codes[i] = __ldg(reinterpret_cast<const uint2*>(src + code));
       else
