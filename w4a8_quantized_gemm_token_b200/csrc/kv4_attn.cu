@@ -13,15 +13,21 @@
 // (a shift by 8 and four masks) a word of 8 codes into four.  The 16 goes into q
 // (K) or into the end of the sums (V).  The other operands are fp16 too:
 //  * q, times a power of two per row that puts its largest element into
-//    [2^13, 2^14): exact, but for elements 2^-23 below the largest;
+//    [2^13, 2^14): exact, but for elements 2^-23 below the largest; sum(q_g) in three
+//    pieces (33 bits), columns of one more product with the offsets;
 //  * P sV: a row's reference is its maximum less what puts the largest P sV of the
 //    record where it was set into [2^9, 2^10); a product of 2^15 or more lowers it in
 //    the same way.  So P sV has 11 bits of significand down to 2^-23 of one that the
 //    row has met, and an error of 2^-34 of that one below.  P oV and l stay in fp32.
 // Sums are fp32 throughout.
 //
-// Bound: HBM (9 D / 8 bytes per visible token and kv head); what has to keep up
-// with it is the issue of instructions, about 220 per record of 16 tokens and warp.
+// Bound: HBM (9 D / 8 bytes per visible token and kv head) and, about as much, the issue
+// of instructions: 239 per record of 16 tokens (D = 128), 83 of them the unpacking.  64
+// requests of 16384 tokens, 8 kv heads: 1.21 GB in 201 us (92 % of the copy rate) at 1965
+// MHz; in a stream of seconds the power limit takes the clock to about 1650 MHz, and the
+// kernel follows it (240 us).  Few records are bound by latency: 9 us for one
+// request of 500 tokens, most of it the loads that depend on one another (lengths,
+// page, record; metas, pieces).
 // mma.sync is used rather than tcgen05 because its operands are registers: a
 // tcgen05 tile of 128 would have to write the unpacked codes to shared memory (2
 // bytes per code written and read, against half a byte loaded) to multiply them
@@ -31,7 +37,7 @@
 //
 // Layout of the work: an item is (request, row tile, kv head), its units are the
 // 16-token records it sees.  All units of all items are laid end to end and cut
-// into equal spans, one per consumer warp, from the lengths on the device: one
+// into equal spans, one per warp, from the lengths on the device: one
 // long request and a ragged batch fill the GPU alike, and no length goes through
 // the host.  A warp that holds a whole item writes the output; the pieces of an
 // item that is cut are joined in the block (through shared memory), and, where
@@ -64,11 +70,13 @@ constexpr int kMaxBlocks = 160;  // a block per SM; the workspace holds this man
 template <int D, int NT>
 struct Cfg {
   static constexpr int ROWS = 8 * NT;
-  // Warps; the registers of the SM over four quarters.  D = 128: 12 of 168 registers, with
-  // two tiles 8 of 255 (12 spill); D = 64: 16 and 12.
+  // Warps; the registers of the SM over four quarters.  D = 128: 12 of 168 registers (15 of
+  // 128 spill a little: 236 us against 231 for 11 of 168, 64 x 16384), with two tiles 8 of
+  // 255 (11 of 168 spill: 70 us against 62, 200 rows over 2500 tokens).  D = 64: 16 and 12,
+  // which spill nothing.
   static constexpr int NW = D == 64 ? (NT == 1 ? 16 : 12) : (NT == 1 ? 12 : 8);
   static constexpr int WINDOW = 32;                    // units numbered at once
-  static constexpr int STAGES = 4;                     // records in a consumer's ring
+  static constexpr int STAGES = 4;                     // records in a warp's ring (six were no faster)
   static constexpr int THREADS = 32 * NW;
   static constexpr int LD = D + 4;                     // floats per row of a piece in shared memory
   static constexpr int PIECE = (ROWS * LD + 2 * ROWS) * 4;  // O rows, then every row's (m, l)
@@ -96,8 +104,8 @@ struct Args {
   int* err;
 };
 
-// ---- workspace: header, a word per block, then two pieces per block (its first
-// item's, where that began in an earlier block, and its last's)
+// ---- workspace: the number of blocks with work, a Meta per block, then two pieces per block
+// (of its first item, where that began in an earlier block, and of its last)
 struct Meta {
   int flags;  // 1: a first piece, 2: it ends its item, 4: a last piece, of
   int rt, kvh, row0, n;  // this row tile and kv head of the request with these rows
@@ -173,7 +181,7 @@ __device__ __forceinline__ void next_item(const Args& a, Item& it) {
   load_tile<ROWS>(a, it);
 }
 
-__device__ __forceinline__ int warp_sum(int v) {
+__device__ __forceinline__ uint32_t warp_sum(uint32_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
@@ -186,10 +194,10 @@ __device__ __forceinline__ long long request_units(const Args& a, const Item& ba
   for (int rt0 = 0; rt0 < base.nrt; rt0 += 32) {
     Item it = base;
     it.rt = rt0 + (threadIdx.x & 31);
-    int c = 0;
+    uint32_t c = 0;
     if (it.rt < it.nrt) {
       load_tile<ROWS>(a, it);
-      c = it.cnt;
+      c = (uint32_t)it.cnt;  // (at most 2^26)
     }
     sum += warp_sum(c);
   }
@@ -1185,7 +1193,10 @@ cudaError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t H,
   a.out = out;
   a.ws = static_cast<uint8_t*>(workspace);
   a.err = err;
-  // rows of an item: 8 where the batch's average request has no more
+  // Rows of an item: 8 where the batch's average request has no more per kv head, else 16.
+  // 16 requests of 8192 tokens, 4 kv heads of 128: with 8 rows 24.8 us (16 to an item: 33.1),
+  // with 9 33.4 (8 to an item, twice the cache: 40.7), with 16 34.9 (40.9).  Of long
+  // chunks of rows both take the same (200 rows over 2500 tokens: 56.8, 59.4).
   const int64_t rows = a.G * ((req.T + req.B - 1) / req.B);
   const bool wide = rows > 8;
   if (cache.D == 64) return wide ? launch<64, 2>(a, s) : launch<64, 1>(a, s);

@@ -16,6 +16,8 @@
 //
 // Bound: HBM.  2 (x) + 2 (residual) + 2 (h) + 1 (codes) bytes per element, each
 // touched once: u stays in fp32 registers between the maximum and the codes.
+// 16384 rows of 4096: 75.7 us, 95 % of the copy rate; 1111 rows of 5120: 9.7 us (62 %:
+// one wave of blocks, a load, a reduction and a store long); one row 2.4 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
