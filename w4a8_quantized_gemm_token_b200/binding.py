@@ -460,7 +460,7 @@ def qk_rmsnorm_quantize(x, weight=None, residual=None, eps=1e-6, h=None, xq=None
     """x bf16 [M, K] (+ residual) -> (h, xq int8 [M, K], sx fp32 [M], xsum int32 [M, K/64] or
     None): the RMS norm of h = x + residual times weight (fp32 [K]) as codes and scales, for
     qk_w8a8_gemm and qk_w4a8_gemm.  h (bf16) is the new residual stream, None without a residual;
-    h may be x or residual itself."""
+    h may be x or residual itself.  New xq, sx and xsum lie in one allocation."""
     return _block_calls.rmsnorm_quantize(x, weight, residual, eps, h, xq, sx, xsum, with_xsum,
                                          _handle(stream))
 
@@ -486,7 +486,7 @@ def qk_rope(q, k, positions, freq, layout=QK_ROPE_HALF, amplitude=1.0, q_out=Non
             stream=None):
     """Rotary positions on q bf16 [T, H, D] and k bf16 [T, Hkv, D] (or None), positions int32 [T],
     the first 2 len(freq) dims of each head; returns (q_out, k_out).  Rows may be strided; q_out=q
-    (k_out=k) turns them in place."""
+    (k_out=k) turns them in place.  New outputs lie in one allocation."""
     return _block_calls.rope(q, k, positions, freq, layout, amplitude, q_out, k_out, _handle(stream))
 
 
@@ -507,7 +507,8 @@ def qk_kv4_append(k, v, cache, page_table, kv_lens, cu_rows=None, stream=None):
 
 def qk_kv4_gather(cache, page_table, kv_lens, cu_rows, T, k=None, v=None, stream=None):
     """(k, v) bf16 [T, Hkv, D]: the values of the last tokens of each request (cu_rows as in
-    qk_kv4_append; all of them where a request's rows number its length)."""
+    qk_kv4_append; all of them where a request's rows number its length).  New k and v lie in
+    one allocation."""
     return _block_calls.kv4_gather(cache, page_table, kv_lens, cu_rows, T, k, v, _handle(stream))
 
 

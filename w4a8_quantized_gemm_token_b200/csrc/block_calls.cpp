@@ -4,7 +4,7 @@
 // Such a call's kernels take 2 to 5 us; checking a dozen tensors, allocating the
 // outputs and converting twenty ctypes arguments in Python takes 10 to 20.  The
 // same checks, with the same exceptions, and the allocations are made here, and
-// the C calls of include/qk.h with the raw pointers: 4 to 7 us with the launches.
+// the C calls of include/qk.h with the raw pointers: 3 to 7 us with the launches (2.4 us each).
 // Nothing is computed here.
 #include <Python.h>
 
@@ -15,6 +15,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <string>
 
@@ -96,6 +97,47 @@ int64_t rows(const Tensor& t, int64_t heads, int64_t D, const char* name) {
     value_error(string(name) + ": a row's heads must be contiguous");
   return t.size(0) > 1 ? t.stride(0) : std::max(heads * D, t.stride(0));
 }
+
+// New contiguous tensors in one allocation, 256 bytes apart: an allocation and its
+// release take 0.8 us, a tensor beside another one 0.15.
+class Together {
+ public:
+  explicit Together(const Tensor& beside) : device_(beside.device()) {}
+  void add(Tensor* out, std::initializer_list<int64_t> shape, ScalarType dtype) {
+    Part& p = parts_[n_++];
+    p = {out, {}, (int)shape.size(), dtype, bytes_};
+    int64_t count = 1;
+    std::copy(shape.begin(), shape.end(), p.shape);
+    for (int64_t x : shape) count *= x;
+    bytes_ += (count * (int64_t)c10::elementSize(dtype) + 255) / 256 * 256;
+  }
+  void make() {
+    if (n_ == 0) return;
+    const int64_t one = 1;
+    const at::TensorBase all = at::detail::empty_strided_cuda(bytes_, one, ScalarType::Byte, device_);
+    for (int i = 0; i < n_; ++i) {
+      const Part& p = parts_[i];
+      auto impl = c10::make_intrusive<at::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                      c10::scalarTypeToTypeMeta(p.dtype));
+      impl->set_sizes_contiguous(at::IntArrayRef(p.shape, p.dims));
+      impl->set_storage_offset(p.at / (int64_t)c10::elementSize(p.dtype));
+      *p.out = Tensor(std::move(impl));
+    }
+  }
+
+ private:
+  struct Part {
+    Tensor* out;
+    int64_t shape[3];
+    int dims;
+    ScalarType dtype;
+    int64_t at;
+  };
+  Part parts_[3];
+  int n_ = 0;
+  int64_t bytes_ = 0;
+  at::Device device_;
+};
 
 const Tensor& rows_of_three(PyObject* o, const char* name, const char* shape) {
   if (!THPVariable_Check(o) || THPVariable_Unpack(o).dim() != 3)
@@ -186,11 +228,20 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   } else if (a[4] != Py_None) {
     value_error("h is written with a residual only");
   }
-  const Tensor xq = output(a[5], {M, K}, ScalarType::Char, x, "xq");
-  const Tensor sx = output(a[6], {M}, ScalarType::Float, x, "sx");
   const int sums = PyObject_IsTrue(a[8]);
   if (sums < 0) throw python_error();
-  if (sums || a[7] != Py_None) xsum = output(a[7], {M, K / 64}, ScalarType::Int, x, "xsum");
+  Tensor xq, sx;  // (used and released together, and with the sums)
+  Together fresh(x);
+  auto take = [&](PyObject* o, Tensor* t, std::initializer_list<int64_t> shape, ScalarType dtype, const char* name) {
+    if (o == Py_None)
+      fresh.add(t, shape, dtype);
+    else
+      *t = output(o, shape, dtype, x, name);
+  };
+  take(a[5], &xq, {M, K}, ScalarType::Char, "xq");
+  take(a[6], &sx, {M}, ScalarType::Float, "sx");
+  if (sums || a[7] != Py_None) take(a[7], &xsum, {M, K / 64}, ScalarType::Int, "xsum");
+  fresh.make();
   same_device(x, weight, residual, h, xq, sx, xsum);
   check(qk_rmsnorm_quantize(ptr<uint16_t>(x), ptr<uint16_t>(residual), M, K, ptr<float>(weight),
                             (float)number(a[3]), ptr<uint16_t>(h), ptr<int8_t>(xq), ptr<float>(sx),
@@ -211,24 +262,28 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& freq = need(a[3], ScalarType::Double, 1, "freq");
   if (positions.size(0) != T) value_error("positions must have shape [" + std::to_string(T) + "]");
   Tensor k, q_out, k_out;
-  auto out = [](PyObject* o, const Tensor& like, const char* name, int64_t* stride) {
-    const int64_t t = like.size(0), heads = like.size(1), d = like.size(2);
-    *stride = heads * d;
-    if (o == Py_None) return output(o, {t, heads, d}, ScalarType::BFloat16, like, name);
-    const Tensor& given = tensor(o, name);
-    *stride = rows(given, heads, d, name);
-    return given;
+  Together fresh(q);
+  auto out = [&](PyObject* o, Tensor* t, const Tensor& like, const char* name, int64_t* stride) {
+    const int64_t heads = like.size(1);
+    *stride = heads * D;
+    if (o == Py_None) {
+      fresh.add(t, {like.size(0), heads, D}, ScalarType::BFloat16);
+    } else {
+      *t = tensor(o, name);
+      *stride = rows(*t, heads, D, name);
+    }
   };
   int64_t qos, Hkv = 0, ks = 0, kos = 0;
-  q_out = out(a[6], q, "q_out", &qos);
+  out(a[6], &q_out, q, "q_out", &qos);
   if (a[1] != Py_None) {
     k = rows_of_three(a[1], "k", "[T, Hkv, D]");
     Hkv = k.size(1);
     ks = rows(k, Hkv, D, "k");
-    k_out = out(a[7], k, "k_out", &kos);
+    out(a[7], &k_out, k, "k_out", &kos);
   } else if (a[7] != Py_None) {
     value_error("k_out without k");
   }
+  fresh.make();
   if (q_out.size(0) != T || (k.defined() && (k.size(0) != T || k_out.size(0) != T)))
     value_error("q, k and the outputs must have the same number of rows");
   same_device(q, k, positions, freq, q_out, k_out);
@@ -293,15 +348,21 @@ PyObject* kv4_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t T = integer(a[4]);
   if (T < 0) value_error("T must not be negative");
   const Cache c(a[0], a[1], a[2], a[3], T);
-  auto out = [&](PyObject* o, const char* name, int64_t* stride) {
+  Together fresh(c.cache);
+  auto out = [&](PyObject* o, Tensor* t, const char* name, int64_t* stride) {
     *stride = c.Hkv * c.D;
-    if (o == Py_None) return output(o, {T, c.Hkv, c.D}, ScalarType::BFloat16, c.cache, name);
-    const Tensor& given = tensor(o, name);
-    *stride = rows(given, c.Hkv, c.D, name);
-    return given;
+    if (o == Py_None) {
+      fresh.add(t, {T, c.Hkv, c.D}, ScalarType::BFloat16);
+    } else {
+      *t = tensor(o, name);
+      *stride = rows(*t, c.Hkv, c.D, name);
+    }
   };
   int64_t ks, vs;
-  const Tensor k = out(a[5], "k", &ks), v = out(a[6], "v", &vs);
+  Tensor k, v;
+  out(a[5], &k, "k", &ks);
+  out(a[6], &v, "v", &vs);
+  fresh.make();
   if (k.size(0) != T || v.size(0) != T) value_error("k and v must have " + std::to_string(T) + " rows");
   same_device(k, v, c.cache, c.table, c.lens, c.cu);
   check(qk_kv4_gather(ptr<void>(c.cache), c.num_pages, c.page, c.Hkv, c.D, ptr<int32_t>(c.table), c.B,
