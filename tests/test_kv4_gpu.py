@@ -1,5 +1,9 @@
 """GPU parity of the 4-bit paged cache and its attention against their formulas in 64 bits, and the
 ways they are called: ragged and padded batches, bad indices, graphs, streams, a block's run."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -509,6 +513,34 @@ def test_graph_replays_with_new_lengths(qk):  # noqa: F811
                 want, tol = ref.attention(q[b:b + 1], kk, vv, D ** -0.5, window, 0)
                 assert ((o[b:b + 1].double() - want).abs() <= tol).all()
     qk.qk_check_device_error()
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls of the library are captured: a step's five calls and the frequencies."""
+    code = (
+        "import torch\n"
+        "from w4a8_quantized_gemm_token_b200 import binding as qk\n"
+        "t = lambda v: torch.tensor(v, dtype=torch.int32, device='cuda')\n"
+        "r = lambda *s: torch.randn(*s, device='cuda').bfloat16()\n"
+        "x, q, k, v = r(4, 256), r(4, 8, 64), r(4, 2, 64), r(4, 2, 64)\n"
+        "pos, table, lens = t([0, 1, 2, 3]), t([[0], [1], [2], [3]]), t([1, 1, 1, 1])\n"
+        "cache = torch.zeros(4, 2, 16, 72, dtype=torch.uint8, device='cuda')\n"
+        "g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g):\n"
+        "    h, xq, sx, xsum = qk.qk_rmsnorm_quantize(x, None, x, with_xsum=True)\n"
+        "    a, b = qk.qk_rope(q, k, pos, qk.qk_rope_frequencies(64))\n"
+        "    qk.qk_kv4_append(b, v, cache, table, lens)\n"
+        "    o = qk.qk_kv4_attention(a, cache, table, lens)\n"
+        "    _, w = qk.qk_kv4_gather(cache, table, lens, None, 4)\n"
+        "g.replay()\n"
+        "qk.qk_check_device_error()\n"
+        "assert torch.equal(h, x + x)\n"
+        "d = (o.view(4, 2, 4, 64).float() - w[:, :, None].float()).abs()\n"
+        "assert (d <= 2.0 ** -7 * w[:, :, None].float().abs() + 1e-3).all()\n"  # one key: two roundings to bf16
+    )
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
 
 
 def test_two_streams_at_once(qk):  # noqa: F811

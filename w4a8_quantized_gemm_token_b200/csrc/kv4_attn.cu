@@ -72,9 +72,11 @@ struct Cfg {
   static constexpr int ROWS = 8 * NT;
   // Warps; the registers of the SM over four quarters.  D = 128: 12 of 168 registers (15 of
   // 128 spill a little: 236 us against 231 for 11 of 168, 64 x 16384), with two tiles 8 of
-  // 255 (11 of 168 spill: 70 us against 62, 200 rows over 2500 tokens).  D = 64: 16 and 12,
-  // which spill nothing.
-  static constexpr int NW = D == 64 ? (NT == 1 ? 16 : 12) : (NT == 1 ? 12 : 8);
+  // 255 (11 of 168 spill: 70 us against 62, 200 rows over 2500 tokens).  D = 64: 16
+  // of 122 (12: 42.4 us against 40.5, 32 requests of 16384), with two tiles 8 of 207 (12
+  // of 168: the same on long batches, 10.0 us against 8.9 on 4 requests of 500: what the
+  // block leaves free of the SM lets the join's blocks start beside it).
+  static constexpr int NW = D == 64 ? (NT == 1 ? 16 : 8) : (NT == 1 ? 12 : 8);
   static constexpr int WINDOW = 32;                    // units numbered at once
   static constexpr int STAGES = 4;                     // records in a warp's ring (six were no faster)
   static constexpr int THREADS = 32 * NW;
