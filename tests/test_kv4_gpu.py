@@ -306,9 +306,9 @@ def test_value_scales_far_apart(qk, D, G):  # noqa: F811
                 want, _ = ref.attention(rows, kk, vv, D ** -0.5, 0, 0)
                 part, _ = ref.attention(rows, kk, reach, D ** -0.5, 0, 0)  # sum P (15 scale + |offset|)
                 a = 3 * D ** -0.5 * rows.double().abs().sum(-1).amax() * kk.abs().amax()
-                # P scale as fp16: 2^-11 of itself, or 2^-25 where the row's largest is at least 2^9: m
-                # times 2^-34 of the largest; scores (2^-17 a each way), 2^x, fp32 sums as in ref.attention
-                move = 2.0 ** -11 + m * 2.0 ** -34 + 2 * a * 2.0 ** -17 + 2.0 ** -20 + (m / 8 + 400) * 2.0 ** -23
+                # P scale as fp16: 2^-11 of itself, or 2^-25 where the row's largest is at least 2^5: m
+                # times 2^-30 of the largest; scores (2^-17 a each way), 2^x, fp32 sums as in ref.attention
+                move = 2.0 ** -11 + m * 2.0 ** -30 + 2 * a * 2.0 ** -17 + 2.0 ** -20 + (m / 8 + 400) * 2.0 ** -23
                 got = out[c.first[b]:c.first[b + 1]].double()
                 assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + part * move).all(), (trend, strength, b)
     qk.qk_check_device_error()

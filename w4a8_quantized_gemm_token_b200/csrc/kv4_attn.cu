@@ -16,9 +16,10 @@
 //    [2^13, 2^14): exact, but for elements 2^-23 below the largest; sum(q_g) in three
 //    pieces (33 bits), columns of one more product with the offsets;
 //  * P sV: a row's reference is its maximum less what puts the largest P sV of the
-//    record where it was set into [2^9, 2^10); a product of 2^15 or more lowers it in
-//    the same way.  So P sV has 11 bits of significand down to 2^-23 of one that the
-//    row has met, and an error of 2^-34 of that one below.  P oV and l stay in fp32.
+//    record where it was set into [2^5, 2^6); a score 2^8 above that maximum sets it
+//    anew, and so does a product of 2^15.  So P sV has 11 bits of significand down to
+//    2^-19 of one that the row has met, and an error of 2^-30 of that one below.  P oV
+//    and l stay in fp32.
 // Sums are fp32 throughout.
 //
 // Bound: HBM (9 D / 8 bytes per visible token and kv head) and, about as much, the issue
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
         }
       }
       // nm: minus the reference, in units of log2; lim: the score that moves it (the
-      // maximum and 2^4); o: rows g (even dims) and g + 8 (odd dims, 16-fold)
+      // maximum and 2^8); o: rows g (even dims) and g + 8 (odd dims, 16-fold)
       float nm[NT][2], lim[NT][2], l[NT][2], off[NT][2][NG], o[NT][NG][2][2][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -671,6 +672,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
       const int stop = it.cnt - k <= room ? it.cnt : k + room;
       const bool ends = stop == it.cnt;
       // A record: kMask where a row may not see all of its keys, dead where it is not there.
+      bool fresh = true;  // nothing is summed yet
       auto step = [&](auto masks, int record, bool dead, bool more) {
         constexpr bool kMask = decltype(masks)::value;
         copies_wait<STAGES - 1>();
@@ -749,7 +751,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
         ++asked;
         place = place == (STAGES - 1) * L::REC ? 0 : place + L::REC;
         // ---- weights, and times scales, as the second product's operand.  A row's reference
-        // moves where a score passes the last maximum by 2^4, or a product comes to 2^15 (the
+        // moves where a score passes the last maximum by 2^8, or a product comes to 2^15 (the
         // half then carries into its sign bit)
         uint32_t w[NT][NG][2];
         float y[NT][4];
@@ -789,20 +791,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
               const float heavy = column_max(fmaxf(ex2((x[n][c] - top) * R[n][c]) * m0,
                                                    ex2((x[n][2 + c] - top) * R[n][c]) * m1));
               const float was = nm[n][c];
-              const float set = (float)(9 - exponent(fmaxf(heavy, 0x1p-24f))) - fmaxf(top * R[n][c], kLeast);
+              const float set = (float)(5 - exponent(fmaxf(heavy, 0x1p-24f))) - fmaxf(top * R[n][c], kLeast);
               if (top > lim[n][c]) {
                 nm[n][c] = set;
-                lim[n][c] = top + 4.0f / R[n][c];
-              } else if (top > -INFINITY && set < nm[n][c] - 4.0f) {
+                lim[n][c] = top + 8.0f / R[n][c];
+              } else if (top > -INFINITY && set < nm[n][c] - 8.0f) {
                 nm[n][c] = set;  // products of 2^13 and more
               }
               alpha[c] = ex2(nm[n][c] - was);
             }
-            rescale(n, alpha);
+            if (!fresh) rescale(n, alpha);
           }
           exponentials();
           weights();
         }
+        fresh = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           l[n][0] += y[n][0] + y[n][2];
