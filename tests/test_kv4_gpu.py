@@ -639,3 +639,31 @@ def test_decode_steps_of_a_block(qk, tokens):  # noqa: F811
     hr, cr, _ = ref.rmsnorm_quantize(update, w2, stream, 1e-6)
     assert torch.equal(bits(h), bits(hr)) and torch.equal(xq, cr)
     qk.qk_check_device_error()
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_all_the_weight_on_a_value_of_scale_zero(qk, rows):  # noqa: F811
+    """One key has all the weight but 2^-50, and a value group that is constant (scale 0): what the other
+    keys add keeps its precision."""
+    lens = [300] * 6
+    c = Batch(qk, lens, [rows] * 6, 16, 64, 16, fill=False)
+    k, v = 0.1 * c.randn(1800, 16, 64), c.randn(1800, 16, 64)
+    k[5::300], v[5::300] = 4.5, 0.0
+    k[5::300, :, 0] = 3.5
+    k, v = k.bfloat16(), v.bfloat16()
+    qk.qk_kv4_append(k, v, c.cache, c.table, c.lens, i32(list(range(0, 1801, 300))))
+    q = torch.ones(c.T, 48, 64, dtype=torch.bfloat16, device="cuda")
+    out = qk.qk_kv4_attention(q, c.cache, c.table, c.lens, c.cu)
+    for b in range(6):
+        kk, vv = ref.request_kv(c.cache, c.table[b], 300, 64)
+        _, _, s, o = ref.quantize4(v[300 * b:300 * b + 300])
+        mine = q[c.first[b]:c.first[b + 1]]
+        want, _ = ref.attention(mine, kk, vv, 0.125, 0, 0)
+        part, _ = ref.attention(mine, kk, (15 * s + o.abs()).repeat_interleave(64, -1), 0.125, 0, 0)
+        assert 0 < part.max() < 2.0 ** -40
+        a = 3 * 0.125 * 64 * kk.abs().amax()
+        # as in test_value_scales_far_apart
+        move = 2.0 ** -11 + 300 * 2.0 ** -30 + 2 * a * 2.0 ** -17 + 2.0 ** -20 + 440 * 2.0 ** -23
+        got = out[c.first[b]:c.first[b + 1]].double()
+        assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + part * move).all()
+    qk.qk_check_device_error()

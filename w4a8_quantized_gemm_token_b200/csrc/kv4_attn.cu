@@ -16,7 +16,8 @@
 //    [2^13, 2^14): exact, but for elements 2^-23 below the largest; sum(q_g) in three
 //    pieces (33 bits), columns of one more product with the offsets;
 //  * P sV: a row's reference is its maximum less what puts the largest P sV of the
-//    record where it was set into [2^5, 2^6); a score 2^8 above that maximum sets it
+//    record where it was set into [2^5, 2^6) (or the maximum's weight to 2^69, where
+//    only values of scale 0 have much of it); a score 2^8 above that maximum sets it
 //    anew, and so does a product of 2^15.  So P sV has 11 bits of significand down to
 //    2^-19 of one that the row has met, and an error of 2^-30 of that one below.  P oV
 //    and l stay in fp32.
@@ -58,14 +59,12 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "fast_div.cuh"
-#include "kv4.cuh"
+#include "kv4_chunk.h"
+#include "kv4_items.cuh"
 #include "sm100.cuh"
 
 namespace qk {
 namespace {
-
-constexpr int kMaxBlocks = 160;  // a block per SM; the workspace holds this many
 
 // NT tiles of 8 query rows per item.
 template <int D, int NT>
@@ -93,20 +92,6 @@ struct Cfg {
   static_assert(SMEM + 24 * (THREADS + 64) <= 232448, "with the static shared memory");
 };
 
-struct Args {
-  const uint16_t* q;
-  long long q_stride;
-  int H, G;
-  FastDiv by_g, by_page;  // rows per token; records per page
-  Kv4Req req;
-  Kv4Cache cache;
-  float sc;  // scale log2 e
-  int window, sinks;
-  uint16_t* out;
-  uint8_t* ws;
-  int* err;
-};
-
 // ---- workspace: the number of blocks with work, a Meta per block, then two pieces per block
 // (of its first item, where that began in an earlier block, and of its last)
 struct Meta {
@@ -123,101 +108,17 @@ __device__ __forceinline__ float* piece_at(uint8_t* ws, int D, int block, int wh
   return reinterpret_cast<float*>(ws + kPieceOff) + (size_t)(2 * block + which) * piece_floats(D);
 }
 
-// ---- items
-
-struct Item {
-  int b, rt, kvh;
-  int row0, n, len, nrt;
-  int cnt, ns, first;  // units, how many of them are sinks' records, first record behind those
-  int p0, p1;          // positions of the tile's first and last row
-  int whole0, whole1;  // every row sees all 16 keys of units [whole0, whole1)
-};
-
-template <int ROWS>
-__device__ __forceinline__ void set_request(const Args& a, Item& it, const Kv4Seq& s) {
-  it.row0 = s.row0;
-  it.n = s.n;
-  it.len = s.len;
-  it.nrt = (s.n * a.G + ROWS - 1) / ROWS;
-}
-
-template <int ROWS>
-__device__ __forceinline__ void load_request(const Args& a, Item& it) {
-  set_request<ROWS>(a, it, kv4_seq(a.req, it.b, a.err));
-}
-
-// The records that row tile rt of the request sees; one empty unit where it sees none.
-template <int ROWS>
-__device__ __forceinline__ void load_tile(const Args& a, Item& it) {
-  const int last = it.n * a.G - 1;
-  it.p0 = it.len - it.n + quot(it.rt * ROWS, a.by_g);
-  it.p1 = it.len - it.n + quot(min(it.rt * ROWS + ROWS - 1, last), a.by_g);
-  it.ns = it.first = it.whole0 = it.whole1 = 0;
-  it.cnt = 1;
-  if (it.p1 < 0) return;
-  const int end = (it.p1 >> 4) + 1;
-  if (a.window > 0) {
-    it.first = max(it.p0 - a.window + 1, 0) >> 4;
-    it.ns = min((a.sinks + 15) >> 4, it.first);
-    it.whole0 = it.ns + ((max(it.p1 - a.window + 1, 0) + 15) >> 4) - it.first;
-  }
-  it.cnt = it.ns + end - it.first;
-  it.whole1 = max(it.ns + ((max(it.p0, -1) + 1) >> 4) - it.first, it.whole0);
-}
-
-__device__ __forceinline__ int record_of(const Item& it, int k) {
-  return k < it.ns ? k : it.first + k - it.ns;
-}
-
-// Steps to the next item (kv heads innermost, then row tiles, then requests).
-template <int ROWS>
-__device__ __forceinline__ void next_item(const Args& a, Item& it) {
-  if (++it.kvh < a.cache.Hkv) return;
-  it.kvh = 0;
-  if (++it.rt >= it.nrt) {
-    it.rt = 0;
-    do {
-      if (++it.b >= a.req.B) return;  // behind the last span
-      load_request<ROWS>(a, it);
-    } while (it.nrt == 0);
-  }
-  load_tile<ROWS>(a, it);
-}
-
-__device__ __forceinline__ uint32_t warp_sum(uint32_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-
-// Units of all row tiles of the request, for one kv head, by the whole warp.
-template <int ROWS>
-__device__ __forceinline__ long long request_units(const Args& a, const Item& base) {
-  long long sum = 0;
-  for (int rt0 = 0; rt0 < base.nrt; rt0 += 32) {
-    Item it = base;
-    it.rt = rt0 + (threadIdx.x & 31);
-    uint32_t c = 0;
-    if (it.rt < it.nrt) {
-      load_tile<ROWS>(a, it);
-      c = (uint32_t)it.cnt;  // (at most 2^26)
-    }
-    sum += warp_sum(c);
-  }
-  return sum;
-}
-
 constexpr uint32_t kNoRecord = 0xFFFFFFFFu;
 
 // Record number (over the whole cache) of unit k of an item, from the id of its page.
-__device__ __forceinline__ int page_of(const Args& a, const Item& it, int k) {
+__device__ __forceinline__ int page_of(const Kv4Args& a, const Item& it, int k) {
   return quot(record_of(it, k), a.by_page);
 }
-__device__ __forceinline__ int page_id(const Args& a, const Item& it, int k) {
+__device__ __forceinline__ int page_id(const Kv4Args& a, const Item& it, int k) {
   if (it.p1 < 0) return 0;  // (an empty unit)
   return __ldg(a.req.page_table + (long long)it.b * a.req.max_pages + page_of(a, it, k));
 }
-__device__ __forceinline__ uint32_t record_number(const Args& a, const Item& it, int k, int id) {
+__device__ __forceinline__ uint32_t record_number(const Kv4Args& a, const Item& it, int k, int id) {
   if (it.p1 < 0) return kNoRecord;
   if (id < 0 || id >= a.cache.num_pages) {
     record_index(a.err);
@@ -329,15 +230,13 @@ __device__ __forceinline__ void weigh(const float (&p)[4], float s0, float s1, u
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const Args a) {
+__global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const Kv4Args a) {
   using C = Cfg<D, NT>;
   using L = Kv4<D>;
   constexpr int NG = L::NG, ROWS = C::ROWS, NW = C::NW, STAGES = C::STAGES, WINDOW = C::WINDOW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem<128>(smem_raw);
-  __shared__ long long pre[C::THREADS + 1];
-  __shared__ Kv4Seq seqs[C::THREADS];
-  __shared__ long long tot[NW];
+  __shared__ Kv4Scan<NW> scan;
   __shared__ int seg_flags[32];
   __shared__ __align__(16) int seg_item[NW][4];  // last piece's rt, kvh, row0, n
   __shared__ __align__(16) int ahead[NW][4];     // the next unit to be numbered: b, rt, kvh, unit of the item
@@ -348,56 +247,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- units in all: a stretch of requests per thread, then a scan over threads
+  // ---- units in all
   const int per = (a.req.B + C::THREADS - 1) / C::THREADS;
-  {
-    long long mine = 0;
-    for (int i = 0; i < per; ++i) {
-      Item it;
-      it.b = threadIdx.x * per + i;
-      it.nrt = 0;
-      int one = 0;
-      if (it.b < a.req.B) {
-        const Kv4Seq sq = kv4_seq(a.req, it.b, a.err);
-        if (i == 0) seqs[threadIdx.x] = sq;  // the stretch's first request
-        set_request<ROWS>(a, it, sq);
-        if (it.nrt == 1) {
-          it.rt = 0;
-          load_tile<ROWS>(a, it);
-          one = it.cnt;
-        }
-      }
-      long long u = one;
-      uint32_t many = __ballot_sync(0xFFFFFFFFu, it.nrt > 1);
-      while (many) {  // requests of several row tiles: the warp counts them together
-        const int src = __ffs(many) - 1;
-        many &= many - 1;
-        Item big;
-        big.n = __shfl_sync(0xFFFFFFFFu, it.n, src);
-        big.len = __shfl_sync(0xFFFFFFFFu, it.len, src);
-        big.nrt = __shfl_sync(0xFFFFFFFFu, it.nrt, src);
-        const long long s = request_units<ROWS>(a, big);
-        if (lane == src) u = s;
-      }
-      mine += u * a.cache.Hkv;
-    }
-    // inclusive scan over the warp, then over the warps
-    long long sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    if (lane == 31) tot[warp] = sum;
-    __syncthreads();
-    long long before = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) before += w < warp ? tot[w] : 0;
-    pre[threadIdx.x + 1] = before + sum;
-    if (threadIdx.x == 0) pre[0] = 0;
-    __syncthreads();
-  }
-  const long long W = pre[C::THREADS];
+  scan_units<ROWS, 4>(a, scan, per, warp);
+  const long long W = scan.pre[C::THREADS];
   // Where there are fewer units than warps, a unit to a warp; where there are less than
   // twice as many, two to a warp, and fewer blocks (257 units of 8 items: 8.9 us against 9.9
   // with two; 2056 units of 8: 11.2 us against 11.5 with one and some warps with two).
@@ -440,54 +293,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
     if (hours) record_timeout(a.err);
     units = hours ? 0 : (int)all;
     if (units > 0) {
-      // the last t with pre[t] <= u0 (it has units): among every NW-th, then among those
-      // behind it
-      int lo = (__popc(__ballot_sync(0xFFFFFFFFu, pre[lane * NW] <= u0)) - 1) * NW;
-      lo += __popc(__ballot_sync(0xFFFFFFFFu, lane < NW && pre[lo + min(lane, NW - 1)] <= u0)) - 1;
-      long long rest = u0 - pre[lo];
-      it.b = lo * per;
-      set_request<ROWS>(a, it, seqs[lo]);
-      if (per > 1) {
-        for (;;) {
-          const long long u = request_units<ROWS>(a, it) * a.cache.Hkv;
-          if (rest < u || it.b + 1 >= a.req.B) break;
-          rest -= u;
-          ++it.b;
-          load_request<ROWS>(a, it);
-        }
-      }
-      int at = 0;  // the row tile
-      for (int rt0 = 0; it.nrt > 1; rt0 += 32) {
-        Item one = it;
-        one.rt = rt0 + lane;
-        long long c = 0;
-        if (one.rt < one.nrt) {
-          load_tile<ROWS>(a, one);
-          c = (long long)one.cnt * a.cache.Hkv;
-        }
-        long long sum = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-          if (lane >= o) sum += v;
-        }
-        const uint32_t over = __ballot_sync(0xFFFFFFFFu, sum > rest);
-        if (over != 0) {
-          const int src = __ffs(over) - 1;
-          rest -= __shfl_sync(0xFFFFFFFFu, sum - c, src);
-          at = rt0 + src;
-          break;
-        }
-        rest -= __shfl_sync(0xFFFFFFFFu, sum, 31);
-        if (rt0 + 32 >= it.nrt) {  // not reached: the units add up
-          units = 0;
-          break;
-        }
-      }
-      it.rt = at;
-      load_tile<ROWS>(a, it);
-      it.kvh = rest >> 31 ? (int)(rest / it.cnt) : (int)((uint32_t)rest / (uint32_t)it.cnt);
-      k = (int)(rest - (long long)it.kvh * it.cnt);
+      if (!locate_unit<ROWS, 4>(a, scan, per, u0, it, k)) units = 0;
       // (the ids of the first pages are on their way while the queries' addresses are made)
       if (it.p1 >= 0 && k + lane < it.cnt)
         asm volatile("prefetch.global.L1 [%0];" ::"l"(a.req.page_table + (long long)it.b * a.req.max_pages +
@@ -542,7 +348,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
       at.rt = from.y;
       at.kvh = from.z;
       if (per == 1)
-        set_request<ROWS>(a, at, seqs[at.b]);
+        set_request<ROWS>(a, at, scan.seqs[at.b]);
       else
         load_request<ROWS>(a, at);
       load_tile<ROWS>(a, at);
@@ -791,7 +597,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
               const float heavy = column_max(fmaxf(ex2((x[n][c] - top) * R[n][c]) * m0,
                                                    ex2((x[n][2 + c] - top) * R[n][c]) * m1));
               const float was = nm[n][c];
-              const float set = (float)(5 - exponent(fmaxf(heavy, 0x1p-24f))) - fmaxf(top * R[n][c], kLeast);
+              const float set = (float)(5 - exponent(fmaxf(heavy, kLightest))) - fmaxf(top * R[n][c], kLeast);
               if (top > lim[n][c]) {
                 nm[n][c] = set;
                 lim[n][c] = top + 8.0f / R[n][c];
@@ -1055,7 +861,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
 // and then each other's sums.  A launch waits for two loads, one after the other:
 // every block's Meta, and then the pieces' rows with their maxima and sums.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(128) kv4_join_kernel(const Args a) {
+__global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4Args a) {
   constexpr int TPP = D / 4, GROUPS = 128 / TPP, AHEAD = 4;
   __shared__ int flags[kMaxBlocks];
   __shared__ __align__(16) float red[GROUPS][D];
@@ -1143,7 +949,7 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Args a) {
 }
 
 template <int D, int NT>
-cudaError_t launch(const Args& a, cudaStream_t s) {
+cudaError_t launch(const Kv4Args& a, cudaStream_t s) {
   using C = Cfg<D, NT>;
   static bool done[64];
   int dev = 0;
@@ -1174,16 +980,32 @@ cudaError_t launch(const Args& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, C::ROWS>, a);
 }
 
+// Whether kv4_chunk.cu's tiles of 128 rows are the faster ones: where the batch's average
+// request fills three quarters of one per kv head, and there are tiles for most of the SMs.
+// 128 rows a request over 2400 keys, 16 kv heads of 128: 8 requests 67 us (104 here), 4 (64
+// tiles) 42 (59), but over 600 keys 30 (27); 96 rows, 8 requests: 64 (82); 64 rows: 63 (61).
+// 300 rows, 8 kv heads, 4 requests (96 tiles): 54 us over 2400 keys (67), 31 over 600 (28).
+// A prompt of 2048 tokens, 8 kv heads of 4 query heads: 125 us (450).
+bool by_chunks(int64_t T, int64_t B, int64_t H, int64_t Hkv) {
+  const int64_t rows = H / Hkv * ((T + B - 1) / B);
+  return rows >= 96 && B * Hkv * ((rows + 127) / 128) >= 96;
+}
+
 }  // namespace
 
 size_t kv4_attention_workspace(int64_t D) {
+  return kv4_chunk_workspace(D);  // (the larger one)
+}
+
+size_t kv4_attention_workspace(int64_t D, int64_t T, int64_t B, int64_t H, int64_t Hkv) {
+  if (by_chunks(T, B, H, Hkv)) return kv4_chunk_workspace(D);
   return kPieceOff + 2 * kMaxBlocks * piece_floats((int)D) * sizeof(float);
 }
 
 cudaError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t H, const Kv4Req& req,
                                  const Kv4Cache& cache, float scale, int64_t window, int64_t sinks,
                                  uint16_t* out, void* workspace, int* err, cudaStream_t s) {
-  Args a = {};
+  Kv4Args a = {};
   a.q = q;
   a.q_stride = q_stride;
   a.H = (int)H;
@@ -1204,6 +1026,7 @@ cudaError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t H,
   // chunks of rows both take the same (200 rows over 2500 tokens: 56.8, 59.4).
   const int64_t rows = a.G * ((req.T + req.B - 1) / req.B);
   const bool wide = rows > 8;
+  if (by_chunks(req.T, req.B, H, cache.Hkv)) return launch_kv4_chunk(a, s);
   if (cache.D == 64) return wide ? launch<64, 2>(a, s) : launch<64, 1>(a, s);
   return wide ? launch<128, 2>(a, s) : launch<128, 1>(a, s);
 }

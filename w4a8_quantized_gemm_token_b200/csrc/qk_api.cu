@@ -832,8 +832,8 @@ qk_status qk_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64
   if (err == nullptr) return QK_ERR_CUDA;
   void* owned = nullptr;
   if (workspace == nullptr) {
-    if ((st = from_cuda(cudaMallocAsync(&owned, need, stream), "cudaMallocAsync(workspace)")) !=
-        QK_OK)
+    if ((st = from_cuda(cudaMallocAsync(&owned, kv4_attention_workspace(D, T, B, H, Hkv), stream),
+                        "cudaMallocAsync(workspace)")) != QK_OK)
       return st;
     workspace = owned;
   }

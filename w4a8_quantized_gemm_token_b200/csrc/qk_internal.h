@@ -100,7 +100,8 @@ cudaError_t launch_kv4_append(const uint16_t* k, int64_t k_stride, const uint16_
 cudaError_t launch_kv4_gather(const Kv4Req& req, const Kv4Cache& cache, uint16_t* k,
                               int64_t k_stride, uint16_t* v, int64_t v_stride, int* err,
                               cudaStream_t s);
-size_t kv4_attention_workspace(int64_t D);
+size_t kv4_attention_workspace(int64_t D);  // of any call
+size_t kv4_attention_workspace(int64_t D, int64_t T, int64_t B, int64_t H, int64_t Hkv);  // of this one
 cudaError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t H, const Kv4Req& req,
                                  const Kv4Cache& cache, float scale, int64_t window, int64_t sinks,
                                  uint16_t* out, void* workspace, int* err, cudaStream_t s);
