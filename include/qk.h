@@ -599,7 +599,7 @@ qk_status qk_kv4_gather(const void *cache, int64_t num_pages, int64_t page, int6
                         const int32_t *kv_lens, const int32_t *cu_rows, int64_t T, uint16_t *k,
                         int64_t k_stride, uint16_t *v, int64_t v_stride, qk_stream_t stream);
 
-/* Bytes of workspace qk_kv4_attention needs (the same for every batch), or 0
+/* Bytes of workspace qk_kv4_attention needs (enough for every batch: 21 MB at D = 128), or 0
  * for a head dim outside the contract. */
 size_t qk_kv4_attention_workspace_size(int64_t D);
 
@@ -612,7 +612,7 @@ size_t qk_kv4_attention_workspace_size(int64_t D);
  * fp32, the softmax and its sums are fp32, a weight times its value's scale enters
  * the second product as fp16 (11 bits), and out is rounded once to bf16: the
  * error is that rounding plus at most about 2^-11 sum_j P_j 15 scale_j (and the
- * fp32 sums').  Deterministic; a request's result does not depend on the rest
+ * fp32 sums'), for weights times scales down to 2^-83 of the largest weight.  Deterministic; a request's result does not depend on the rest
  * of the batch beyond the order in which its parts are joined.
  *   q         : bf16 bits, row t at q + t q_stride, H heads of D (in)
  *   scale     : finite, >= 0;  window, sinks: >= 0 (window = 0: all keys),
@@ -624,8 +624,10 @@ size_t qk_kv4_attention_workspace_size(int64_t D);
  *               workspaces of their own.  Nothing in it is kept.
  * Pages in front of every row's window (and behind the sinks) are not read and
  * may be freed.  (H / Hkv) T <= 2^30.
- * Kernels: the attention (one block per SM, a warp per equal span of the cache)
- * and the join of what was cut between blocks.
+ * Kernels: the attention (one block per SM, equal spans of the cache to its warps,
+ * or, for many rows per request, to the block: tiles of 128 rows by tcgen05, with the
+ * same precision) and the join of what was cut between blocks.  Which of the two is
+ * decided by T, B and the heads alone.
  */
 qk_status qk_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t T, int64_t H, int64_t Hkv,
                            int64_t D, const void *cache, int64_t num_pages, int64_t page,
