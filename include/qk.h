@@ -612,8 +612,9 @@ size_t qk_kv4_attention_workspace_size(int64_t D);
  * fp32, the softmax and its sums are fp32, a weight times its value's scale enters
  * the second product as fp16 (11 bits), and out is rounded once to bf16: the
  * error is that rounding plus at most about 2^-11 sum_j P_j 15 scale_j (and the
- * fp32 sums'), for weights times scales down to 2^-83 of the largest weight.  Deterministic; a request's result does not depend on the rest
- * of the batch beyond the order in which its parts are joined.
+ * fp32 sums'), for weights times scales down to 2^-83 of the largest weight.
+ * Deterministic; a request's result does not depend on the rest of the batch
+ * beyond the choice of the kernel and the order in which its parts are joined.
  *   q         : bf16 bits, row t at q + t q_stride, H heads of D (in)
  *   scale     : finite, >= 0;  window, sinks: >= 0 (window = 0: all keys),
  *               at most 2^30

@@ -488,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4Args a)
     if (warp == 4) {
       int seg = 0;
       int ns = 0, np = 0;        // stage and its phase of the next scores
-      int vs = 0;                // stage of the next weights
+      int vs = 0, vp = 0;        // stage of the next weights, and its phase
+      int last = -1, last_phase = 0;
       uint32_t turn[2] = {0, 0}; // blocks of each group whose weights were multiplied
 #pragma unroll 1
       for (int n; (n = segment()) > 0;) {
@@ -533,7 +534,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4Args a)
             mma_commit(empty(vs));
           }
           __syncwarp();
-          if (++vs == STAGES) vs = 0;
+          last = vs;
+          last_phase = vp;
+          if (++vs == STAGES) {
+            vs = 0;
+            vp ^= 1;
+          }
           if (i + 2 < n) scores(i + 2);
         }
         ++seg;
@@ -541,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4Args a)
         k = 0;
         next_item<kRows, kLog>(a, it);
       }
+      if (last >= 0) wait(empty(last), last_phase);  // (no arrival is on its way when the block ends)
     }
   } else {
     // -------------------------------------------------------------------- softmax
