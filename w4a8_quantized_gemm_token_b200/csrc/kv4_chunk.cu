@@ -232,8 +232,8 @@ __device__ __forceinline__ float* piece_at(uint8_t* ws, int D, int block, int wh
   return reinterpret_cast<float*>(ws + kPieceOff) + (size_t)(2 * block + which) * piece_floats(D);
 }
 
-// Scales and offsets of a pair of keys.  (fp16 in shared memory: a warp's load of 16 bytes
-// from four places takes four cycles of it, fp32 would take twice as many loads.)
+// Scales and offsets of a pair of keys.  (fp32 in shared memory: as fp16, half the loads and
+// two conversions for each of them, a block of 64 keys took 1.24 us instead of 1.15.)
 template <int NG>
 __device__ __forceinline__ void scales(uint32_t at, uint64_t (&sc)[NG], uint64_t (&of)[NG]) {
 #pragma unroll
