@@ -461,7 +461,8 @@ qk_status qk_sage_attention(const uint16_t *q, const uint16_t *k, const uint16_t
  *   u_k  = fl32(h_k weight_k)                (u = h without a weight)
  *   U    = max_k |u_k|;  rstd = 1 / sqrt(sum_k h_k^2 / K + eps)
  *   xq_k = round-half-even(fl32(u_k fl32(127 fl32(1 / U)))) clamped to [-127, 127]
- *   sx   = fl32(fl32(U / 127) rstd);  an all-zero u gets sx = 1, codes 0
+ *   sx   = fl32(fl32(U / 127) rstd);  an all-zero u gets sx = 1, codes 0;
+ *          a row with a NaN among its u gets sx = NaN, codes 0
  *   xsum[m, g] = sum of the codes of group g of 64, when xsum is not NULL
  * so that xq sx is the norm h rstd weight in 8 bits.  The row's rstd cancels in
  * the codes, which are exact: only sx depends on the fp32 sum of squares.

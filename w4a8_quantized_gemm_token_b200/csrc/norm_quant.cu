@@ -8,6 +8,7 @@
 //     code  = rne(fl32(u_k fl32(127 fl32(1 / U)))), clamped to [-127, 127]
 //     sx    = fl32(fl32(U / 127) rstd),  rstd = 1 / sqrt(sum_k h_k^2 / n + eps)
 //     xsum  = sums of 64 codes                 (when asked for)
+// A NaN among the u_k makes U, and so sx, NaN (and the codes 0), as in act_quant.cuh.
 // The row's 1 / rms multiplies every element alike, so it cancels in the codes
 // (|u| / U has no rms in it) and goes into the scale: one pass over the row
 // decides every code from u, as act_quant.cuh does from x (with the multiplier from
@@ -42,6 +43,13 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// The larger one, NaN where either is: a row's NaN has to reach its scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 __device__ __forceinline__ uint4 add_chunk(uint4 a, uint4 b) {
   return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z),
                     add_bf16x2(a.w, b.w));
@@ -66,7 +74,7 @@ __device__ __forceinline__ void weigh(uint4 h, const float* __restrict__ weight,
     for (int i = 0; i < 8; ++i) u[i] = __fmul_rn(u[i], w[i]);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) *top = fmaxf(*top, fabsf(u[i]));
+  for (int i = 0; i < 8; ++i) *top = max_nan(*top, fabsf(u[i]));
 }
 
 __device__ __forceinline__ uint2 code_chunk(const float (&u)[8], float r, int* sum) {
@@ -150,7 +158,7 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     ssq += __shfl_xor_sync(0xFFFFFFFFu, ssq, o);
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   }
   if constexpr (WPR > 1) {
     if (lane == 0) {
@@ -162,7 +170,7 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
     for (int w = 0; w < WPR; ++w) {
       ssq += red_ssq[(warp / WPR) * WPR + w];
-      top = fmaxf(top, red_top[(warp / WPR) * WPR + w]);
+      top = max_nan(top, red_top[(warp / WPR) * WPR + w]);
     }
   }
   if (!live) return;
