@@ -564,11 +564,14 @@ qk_status qk_rope(const uint16_t *q, int64_t q_stride, uint16_t *q_out, int64_t 
  *                tokens of the request, row r of n at position kv_len - n + r.
  *                NULL: T / B rows each (T % B == 0).  Rows in front of cu_rows[0]
  *                or from cu_rows[B] on belong to nobody and are left alone.
- * The host cannot see these.  A kernel that meets one out of range (a kv_len
- * below 0 or above max_pages page, a row bound outside [0, T] or falling, a
- * page id outside [0, num_pages) under a token that is needed, an appended row at
- * a negative position) records QK_ERR_INDEX for qk_check_device_error and skips
- * that token: nothing outside the buffers is read or written.
+ * The host cannot see these.  A kernel that meets one out of range records
+ * QK_ERR_INDEX for qk_check_device_error, and nothing outside the buffers is read or
+ * written:
+ *   - a kv_len below 0 or above max_pages page, a row bound outside [0, T] or falling:
+ *     the request is skipped.  Its rows within [0, T) append nothing, come back as
+ *     zeros and see no key.
+ *   - a page id outside [0, num_pages) under a token that is needed, a row appended or
+ *     read back at a negative position: that token is skipped.
  * Shape contract: D = 64 or 128; page % 16 == 0, 16 <= page <= 1024;
  * Hkv >= 1; 1 <= num_pages, max_pages; num_pages Hkv page / 16 < 2^32 - 1 (records);
  * max_pages page <= 2^30; T <= 2^30; B >= 1 (T = 0 is a no-op).  16-byte alignment; row strides (in elements) >= heads D

@@ -49,3 +49,45 @@ def test_norm_of_nan(qk, M, K, where):  # noqa: F811
     keep = [m for m in range(M) if m not in rows]
     for a, b in zip((xq, sx, xsum), clean[1:]):
         assert torch.equal(a[keep], b[keep])
+
+
+# ------------------------------------------------------------------------------- lengths and row bounds
+
+@pytest.mark.parametrize("rows", [[2, 1, 3], [100, 90, 120]])
+def test_requests_out_of_range_are_skipped(qk, rows):  # noqa: F811
+    """A request whose length or row bounds are out of range appends nothing, comes back as zeros and sees no
+    key: none of its rows is taken for a row of another position."""
+    D, Hkv = 64, 32
+    c = Batch(qk, [300, 200, 260], rows, Hkv, D, 16, wide=2)
+    most = c.table.shape[1] * c.page
+    a, b, e, T = c.first[0], c.first[1], c.first[2], c.T
+    q = c.q(Hkv)
+    k, v = (c.randn(T, Hkv, D).bfloat16() for _ in range(2))
+    cases = [(i32([300, 200, n]), c.cu, e, T) for n in (most + 1, most + rows[2], 2 ** 31 - 1, -1, -2 ** 31)]
+    cases += [(c.lens, i32([a, b, e, T + n]), e, T) for n in (1, 50, 2 ** 30)]
+    cases += [(c.lens, i32([-1, b, e, T]), a, b), (c.lens, i32([-2 ** 31, b, e, T]), a, b)]
+    for lens, cu, at, end in cases:
+        cache = c.cache.clone()
+        qk.qk_kv4_append(k, v, cache, c.table, lens, cu)
+        with pytest.raises(qk.QKError) as err:
+            qk.qk_check_device_error()
+        assert err.value.status == INDEX
+        # only the other requests' tokens are written
+        want = c.cache.clone()
+        other = [i for i in range(3) if c.first[i] != at]
+        for i in other:
+            s = slice(c.first[i], c.first[i + 1])
+            qk.qk_kv4_append(k[s].contiguous(), v[s].contiguous(), want,
+                             c.table[i:i + 1].clone(), c.lens[i:i + 1].clone())
+        qk.qk_check_device_error()
+        assert torch.equal(cache, want)
+        gk, gv = qk.qk_kv4_gather(want, c.table, lens, cu, T)
+        out = torch.full_like(q, 7.0)
+        qk.qk_kv4_attention(q, c.cache, c.table, lens, cu, out=out)
+        with pytest.raises(qk.QKError) as err:
+            qk.qk_check_device_error()
+        assert err.value.status == INDEX
+        assert not gk[at:end].any() and not gv[at:end].any() and not out[at:end].any()
+        c.check(q, out, requests=other)
+        for i in other:
+            assert gk[c.first[i]:c.first[i + 1]].any()

@@ -42,21 +42,29 @@ struct Kv4Seq {
   int len;   // tokens in the cache, the rows' own included
 };
 
-// Request b's rows and length, held inside the buffers' bounds.
+// Request b's rows and length, held inside the buffers' bounds.  Where they are out of range the
+// request is skipped: its length is 0, so that its rows lie in front of the first token.  (With
+// the clamped length or number of rows they would be rows of other positions.)
 __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4Req& r, int b, int* err) {
   Kv4Seq s;
-  const int len = __ldg(r.kv_lens + b);
+  s.len = __ldg(r.kv_lens + b);
+  int end;
   if (r.cu != nullptr) {
-    const int a = __ldg(r.cu + b), e = __ldg(r.cu + b + 1);
-    s.row0 = min(max(a, 0), r.T);
-    s.n = max(min(e, r.T) - s.row0, 0);
-    if (s.row0 != a || s.row0 + s.n != e) record_index(err);
+    s.row0 = __ldg(r.cu + b);
+    end = __ldg(r.cu + b + 1);
+    s.n = (int)((uint32_t)end - (uint32_t)s.row0);
   } else {
     s.n = r.T / r.B;
     s.row0 = b * s.n;
+    end = s.row0 + s.n;
   }
-  s.len = min(max(len, 0), r.max_len);
-  if (s.len != len) record_index(err);
+  // (as unsigned numbers, the negative ones are too large)
+  if ((uint32_t)s.len > (uint32_t)r.max_len || (uint32_t)s.row0 > (uint32_t)end || (uint32_t)end > (uint32_t)r.T) {
+    s.row0 = min(max(s.row0, 0), r.T);
+    s.n = max(min(end, r.T) - s.row0, 0);
+    s.len = 0;
+    record_index(err);
+  }
   return s;
 }
 
