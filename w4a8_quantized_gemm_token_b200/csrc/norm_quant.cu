@@ -43,10 +43,10 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// The larger one, NaN where either is: a row's NaN has to reach its scale.
-__device__ __forceinline__ float max_nan(float a, float b) {
+// The largest magnitude, NaN where one is: a row's NaN has to reach its scale.
+__device__ __forceinline__ float max_nan(float a, float b, float c = 0.0f) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -74,7 +74,7 @@ __device__ __forceinline__ void weigh(uint4 h, const float* __restrict__ weight,
     for (int i = 0; i < 8; ++i) u[i] = __fmul_rn(u[i], w[i]);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) *top = max_nan(*top, fabsf(u[i]));
+  for (int i = 0; i < 8; i += 2) *top = max_nan(*top, u[i], u[i + 1]);
 }
 
 __device__ __forceinline__ uint2 code_chunk(const float (&u)[8], float r, int* sum) {
@@ -101,8 +101,14 @@ __device__ __forceinline__ float norm_scale(float top, float ssq, int K, float e
 // WPR warps share a row (kWarps / WPR rows per block); a thread holds CPT chunks
 // of 8 elements.  CPT == 0: rows longer than 8 * 256 * 8 elements, read twice
 // (the second time h, from where this thread wrote it, or x).
+//
+// Blocks per SM: what the registers of the chunks allow.  (A row of three chunks and eight warps
+// would take 50, four blocks: 1111 rows of 5120 in 8.8 us; in 48, five blocks and a spilled
+// pointer, 8.7, and 8.5 by a maximum that drops NaN.)
+constexpr int resident(int cpt) { return cpt == 8 ? 2 : cpt == 6 ? 3 : cpt == 4 ? 4 : cpt == 3 ? 5 : 6; }
+
 template <int WPR, int CPT>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, resident(CPT))
     norm_quant_kernel(const uint16_t* x, const uint16_t* residual, int M, int K,
                       const float* __restrict__ weight, float eps, uint16_t* h, int8_t* xq,
                       float* sx, int32_t* xsum) {
