@@ -91,3 +91,25 @@ def test_requests_out_of_range_are_skipped(qk, rows):  # noqa: F811
         c.check(q, out, requests=other)
         for i in other:
             assert gk[c.first[i]:c.first[i + 1]].any()
+
+
+# ------------------------------------------------------------------------------------- sizes of queries
+
+# requests, rows of each: few rows; tiles of 128 rows (16 kv heads, 1 query head)
+FEW, MANY = ([100, 17], [3, 1]), ([150] * 6, [100] * 6)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", [FEW, MANY])
+@pytest.mark.parametrize("power", [104, 113, 117, 121, 124])
+def test_largest_queries(qk, D, shape, power):  # noqa: F811
+    """Rows up to the largest bf16 values, with the scale that brings the scores back (elements of 2^126 and
+    more: neither the rows' sums nor the scores' factor may leave fp32 on the way)."""
+    c = Batch(qk, *shape, 16, D, 16, seed=power)
+    q = (c.randn(c.T, 16, D).clamp(-4, 4) * 2.0 ** power).bfloat16()
+    q[:, 1] = q[:, 1].abs()  # (a row's sum: up to 2^130)
+    scale = D ** -0.5 * 2.0 ** -power
+    out = qk.qk_kv4_attention(q, c.cache, c.table, c.lens, c.cu, scale=scale)
+    # the scale itself comes as fp32, below 2^-126 with fewer bits
+    c.check(q, out, scale=float(np.float32(scale)))
+    qk.qk_check_device_error()

@@ -388,17 +388,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
       for (int n = 0; n < NT; ++n) {
         float top = 0.0f, sum[NG];
 #pragma unroll
-        for (int grp = 0; grp < NG; ++grp) sum[grp] = 0.0f;
-#pragma unroll
         for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint32_t w[4] = {raw[n][grp][j].x, raw[n][grp][j].y, raw[n][grp][j].z, raw[n][grp][j].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              sum[grp] += bf_lo(w[i]) + bf_hi(w[i]);
-              top = fmaxf(top, fmaxf(fabsf(bf_lo(w[i])), fabsf(bf_hi(w[i]))));
-            }
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf_lo(w[i])), fabsf(bf_hi(w[i]))));
           }
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
@@ -407,9 +402,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
         const float f = pow2(-e);
 #pragma unroll
         for (int grp = 0; grp < NG; ++grp) {
+          sum[grp] = 0.0f;  // in the queries' unit: of rows near the largest bf16 it may leave fp32's range
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint4 v = raw[n][grp][j];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[grp] += fmaf(bf_lo(w[i]), f, bf_hi(w[i]) * f);
             qb[n][grp][j][0] = pack_f16(bf_lo(v.x) * f, bf_lo(v.z) * f);
             qb[n][grp][j][1] = pack_f16(bf_hi(v.x) * f * 0.0625f, bf_hi(v.z) * f * 0.0625f);
             qb[n][grp][j][2] = pack_f16(bf_lo(v.y) * f, bf_lo(v.w) * f);
@@ -422,7 +421,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
         float piece[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int grp = 0; grp < NG; ++grp) {
-          float rest = sum[grp] * f * 0x1p-7f;
+          float rest = sum[grp] * 0x1p-7f;
           const float first = __half2float(__float2half_rn(rest));
           rest = t == 0 ? first : rest - first;
           const float second = __half2float(__float2half_rn(rest));
@@ -436,7 +435,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
           const int ec = __shfl_sync(0xFFFFFFFFu, e, from);
           // the scores' unit: x = 2^(24 + e) times what the codes' product gives
           // (neither 0 nor infinite: a masked score is -inf, one of 0 stays 0)
-          R[n][c] = fminf(fmaxf(a.sc * pow2(min(24 + ec, 127)), 1.0e-35f), 3.0e38f);
+          R[n][c] = fminf(fmaxf(a.sc * pow2(ec) * 0x1p24f, 1.0e-35f), 3.0e38f);
           const int rc = it.rt * ROWS + 8 * n + 2 * t + c;
           const int tc = quot(rc, a.by_g);
           pos[n][c] = tc < it.n ? it.len - it.n + tc : -1;

@@ -583,16 +583,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4Args a)
         for (int c = 0; c < N; ++c) {
           const uint32_t v[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sum += bf_lo(v[i]) + bf_hi(v[i]);
-            top = fmaxf(top, fmaxf(fabsf(bf_lo(v[i])), fabsf(bf_hi(v[i]))));
-          }
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf_lo(v[i])), fabsf(bf_hi(v[i]))));
         }
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         // times 2^-e, the largest element comes into [2^13, 2^14)
         const int e = min(max(top == 0.0f ? 0 : exponent(top) - 13, -113), 113);
         const float f = pow2(-e);
-        sum *= f;
+        // (in the queries' unit: of rows near the largest bf16 the sum may leave fp32's range)
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          const uint32_t v[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum += fmaf(bf_lo(v[i]), f, bf_hi(v[i]) * f);
+        }
         const float other = __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
         uint8_t* dst = smem + C::SM_Q + (NG == 2 ? half * C::Q_SLAB : 0) + r * 128;
 #pragma unroll
