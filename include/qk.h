@@ -617,6 +617,9 @@ size_t qk_kv4_attention_workspace_size(int64_t D);
  * the second product as fp16 (11 bits), and out is rounded once to bf16: the
  * error is that rounding plus at most about 2^-11 sum_j P_j 15 scale_j (and the
  * fp32 sums'), for weights times scales down to 2^-83 of the largest weight.
+ * Scores count as far as fp32 holds their differences: a row with a score scale q . k log2 e
+ * of 2^26 or more is NaN (and so may be one whose scores are all below -2^26 over a
+ * stretch of keys), never a wrong number.
  * Deterministic; a request's result does not depend on the rest of the batch
  * beyond the choice of the kernel and the order in which its parts are joined.
  *   q         : bf16 bits, row t at q + t q_stride, H heads of D (in)

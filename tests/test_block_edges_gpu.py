@@ -113,3 +113,46 @@ def test_largest_queries(qk, D, shape, power):  # noqa: F811
     # the scale itself comes as fp32, below 2^-126 with fewer bits
     c.check(q, out, scale=float(np.float32(scale)))
     qk.qk_check_device_error()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", [FEW, MANY])
+def test_scores_of_any_size(qk, D, shape):  # noqa: F811
+    """Scores up to 2^26 (in units of log2) pick the key that is largest; a row with larger ones is NaN, and
+    never the zeros of a row that sees nothing."""
+    c = Batch(qk, *shape, 16, D, 16, fill=False)
+    total = sum(c.lens_list)
+    # key j of a request: -1 everywhere but in dim j % D, which is 1 (every value exact: offset -1, scale 2/15)
+    at = torch.cat([torch.arange(n, device="cuda") for n in c.lens_list]) % D
+    k = torch.full((total, 16, D), -1.0, device="cuda")
+    k[torch.arange(total, device="cuda"), :, at] = 1.0
+    v = torch.randn(total, 16, D, generator=c.g, device="cuda").bfloat16()
+    qk.qk_kv4_append(k.bfloat16(), v, c.cache, c.table, c.lens, i32(np.concatenate([[0], np.cumsum(c.lens_list)])))
+    qk.qk_check_device_error()
+    # a query of one dim: a score of +q where the key's dim is that one, -q elsewhere
+    dim = 3
+    for power in (10, 20, 24, 25, 27, 40, 80, 120, 127):
+        q = torch.zeros(c.T, 16, D, device="cuda")
+        q[:, :, dim] = 1.0
+        q[:, 1, dim] = 2.0 ** power  # (only this head's scores are large)
+        out = qk.qk_kv4_attention(q.bfloat16(), c.cache, c.table, c.lens, c.cu, scale=1.0)
+        qk.qk_check_device_error()
+        for b, (n, L) in enumerate(zip(c.rows_list, c.lens_list)):
+            kk, vv = ref.request_kv(c.cache, c.table[b], L, D)
+            got = out[c.first[b]:c.first[b] + n].double()
+            want, tol = ref.attention(torch.ones(n, 16, D, device="cuda") * (torch.arange(D, device="cuda") == dim),
+                                      kk, vv, 1.0, 0, 0)
+            rest = [h for h in range(16) if h != 1]
+            assert ((got - want).abs() <= tol)[:, rest].all()
+            if power >= 27:
+                assert torch.isnan(got[:, 1]).all(), power
+                continue
+            # the keys of dim `dim` that a row sees, alike; a row that sees none: all of its keys alike
+            key = torch.arange(L, device="cuda")
+            see = key[None] <= torch.arange(L - n, L, device="cuda")[:, None]
+            picked = see & (key % D == dim)[None]
+            p = torch.where(picked.any(1, keepdim=True), picked, see).double()
+            w = (p / p.sum(1, keepdim=True)) @ vv[:, 1]
+            # bf16's rounding, and weight x scale in fp16: 15 scales are within twice the largest value
+            bound = 2.0 ** -8 * w.abs() + (2.0 ** -11 + 2.0 ** -18) * 2 * vv.abs().amax()
+            assert ((got[:, 1] - w).abs() <= bound).all(), power

@@ -179,7 +179,6 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t v) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-__device__ __forceinline__ int exponent(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
 
 // 4 N bytes at a shared address; kOff: more bytes.
 template <int kOff, int N>
@@ -214,7 +213,6 @@ __device__ __forceinline__ float column_max(float v) {
 }
 
 constexpr float kNone = -1.0e30f;   // the reference maximum of a row that has seen nothing
-constexpr float kLeast = -3.0e38f;  // the least one that is kept
 
 // Rows of P sV of 16 keys as fp16 (b0, b1 of the second product, one group).  With
 // masks, a key that a row does not see has weight 0 whatever its record holds.
@@ -596,7 +594,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) kv4_attn_kernel(const 
               const float heavy = column_max(fmaxf(ex2((x[n][c] - top) * R[n][c]) * m0,
                                                    ex2((x[n][2 + c] - top) * R[n][c]) * m1));
               const float was = nm[n][c];
-              const float set = (float)(5 - exponent(fmaxf(heavy, kLightest))) - fmaxf(top * R[n][c], kLeast);
+              const float set = reference(top * R[n][c], heavy);
               if (top > lim[n][c]) {
                 nm[n][c] = set;
                 lim[n][c] = top + 8.0f / R[n][c];

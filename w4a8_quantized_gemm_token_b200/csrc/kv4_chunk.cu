@@ -182,7 +182,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-__device__ __forceinline__ int exponent(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 r = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -216,7 +215,6 @@ __device__ __forceinline__ uint32_t codes(uint32_t w) {
 }
 
 constexpr float kNone = -1.0e30f;   // the reference maximum of a row that has seen nothing
-constexpr float kLeast = -3.0e38f;  // the least one that is kept
 
 // ---- workspace: the number of blocks with work, a Meta per block, two pieces per block (of
 // its first item, where that began in an earlier block, and of its last)
@@ -725,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4Args a)
           for (int i = 0; i < 4; ++i) {
             heavy[i] = quad_max(heavy[i]);
             const float was = nm[i];
-            const float set = (float)(5 - exponent(fmaxf(heavy[i], kLightest))) - fmaxf(most[i] * R[i], kLeast);
+            const float set = reference(most[i] * R[i], heavy[i]);
             // (or products of 2^13 and more)
             const bool above = most[i] > lim[i];
             nm[i] = above | ((most[i] > -INFINITY) & (set < was - 8.0f)) ? set : was;

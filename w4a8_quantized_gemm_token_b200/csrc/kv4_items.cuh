@@ -21,6 +21,20 @@ namespace qk {
 // 2^120.
 constexpr float kLightest = 0x1p-64f;
 
+__device__ __forceinline__ int exponent(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
+
+constexpr float kLeast = -3.0e38f;  // the least maximum that is kept
+
+// The reference that a row's largest score sets (top, in units of log2; heavy: the largest weight
+// times scale if that score's weight is 1): added to the scores, it puts `heavy` into [2^5, 2^6).
+// From |top| = 2^26 on one step of it in fp32 is 8 and more: it would not land there, the products
+// could leave fp16, and fp32 scores hold no difference that a softmax could tell.  Such a row
+// is NaN.
+__device__ __forceinline__ float reference(float top, float heavy) {
+  if (fabsf(top) >= 0x1p26f && top > -INFINITY) return __int_as_float(0x7FFFFFFF);
+  return (float)(5 - exponent(fmaxf(heavy, kLightest))) - fmaxf(top, kLeast);
+}
+
 constexpr int kMaxBlocks = 160;  // a block per SM; the workspace holds this many
 
 struct Kv4Args {
