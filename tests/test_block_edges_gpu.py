@@ -156,3 +156,63 @@ def test_scores_of_any_size(qk, D, shape):  # noqa: F811
             # bf16's rounding, and weight x scale in fp16: 15 scales are within twice the largest value
             bound = 2.0 ** -8 * w.abs() + (2.0 ** -11 + 2.0 ** -18) * 2 * vv.abs().amax()
             assert ((got[:, 1] - w).abs() <= bound).all(), power
+
+
+# ---------------------------------------------------------------------------------------- every key counts
+
+@pytest.mark.parametrize("lens,rows,Hkv,G,D", [
+    ([20000], [1], 2, 4, 128),            # one request over every block
+    ([20000], [1], 1, 12, 64),            # and with two row tiles to an item
+    ([9000, 30, 14000], [1, 1, 1], 1, 8, 64),
+    ([300], [300], 4, 4, 128),
+    ([2100, 40], [700, 40], 2, 3, 64),
+    ([777] * 40, [1] * 40, 8, 5, 128),
+    ([3000] + [1, 17] * 60, [1] + [1, 1] * 60, 2, 8, 128),
+    # in tiles of 128 rows
+    ([2000], [2000], 4, 3, 64),
+    ([5000, 70], [600, 70], 8, 4, 128),
+    ([20000, 30], [4, 30], 8, 64, 128),
+    ([700] + [0] * 6, [700] + [0] * 6, 16, 2, 128),
+])
+def test_every_record_counts(qk, lens, rows, Hkv, G, D):  # noqa: F811
+    """Values of 15 in one dim each, which runs through the records, and 0 elsewhere: an output is a sum of
+    weights without cancellation, so its bound is relative to it, and leaving out any record breaks it."""
+    c = Batch(qk, lens, rows, Hkv, D, 32, fill=False, seed=len(lens))
+    total = sum(lens)
+    k = c.randn(total, Hkv, D).bfloat16()
+    rec = torch.cat([torch.arange(n, device="cuda") // 16 for n in lens])
+    v = torch.zeros(total, Hkv, D, device="cuda")
+    v[torch.arange(total, device="cuda"), :, rec % D] = 15.0
+    qk.qk_kv4_append(k, v.bfloat16(), c.cache, c.table, c.lens, i32(np.concatenate([[0], np.cumsum(lens)])))
+    q = (c.randn(c.T, Hkv * G, D) * 0.3).bfloat16()
+    out = qk.qk_kv4_attention(q, c.cache, c.table, c.lens, c.cu)
+    qk.qk_check_device_error()
+    for b in range(0, len(lens), max(1, len(lens) // 20)):
+        n, L = rows[b], lens[b]
+        if n == 0:
+            continue
+        kk, vv = ref.request_kv(c.cache, c.table[b], L, D)
+        assert ((vv == 15) | (vv == 0)).all()  # scale 1, code 15; a group of zeros has scale 0
+        qb = q[c.first[b]:c.first[b] + n]
+        want, _ = ref.attention(qb, kk, vv, D ** -0.5, 0, 0)
+        got = out[c.first[b]:c.first[b] + n].double()
+        # all terms are >= 0 and each is off by relative amounts: half a step of bf16 2^-8; half a step 2^-11 of
+        # fp16 in the weights; the scores' 2^-17 a (as in block_reference.attention; a: scale times the largest
+        # sum |q| (|code scale| + |offset|), within 3 |k|), in the weights and in their sum; 2^x and the sum of
+        # weights 2^-20; two fp32 roundings per 16 keys and 400 for the joins, above and below
+        a = 3 * D ** -0.5 * (qb.double().abs().sum(-1).amax() * kk.abs().amax()).item()
+        rel = 2.0 ** -8 + 2.0 ** -11 + 4 * a * 2.0 ** -17 + 2.0 ** -19 + 2 * (2 * (L / 16) + 400) * 2.0 ** -24
+        assert rel < 0.011
+        assert ((got - want).abs() <= rel * want).all(), b
+        # without record r its dim keeps 1 - s / B of its sum B, and everything grows by 1 / (1 - s)
+        x = torch.einsum("hd,jhd->hj", qb[-1].double(), kk.repeat_interleave(G, 1)) * D ** -0.5
+        p = torch.softmax(x, 1)
+        R = -(-L // 16)
+        share = torch.zeros(Hkv * G, R, dtype=torch.float64, device="cuda")
+        share.index_add_(1, torch.arange(L, device="cuda") // 16, p)
+        dim = torch.zeros(Hkv * G, D, dtype=torch.float64, device="cuda")
+        dim.index_add_(1, torch.arange(R, device="cuda") % D, share)
+        if R > 1:
+            left = (1 - share / dim[:, torch.arange(R, device="cuda") % D]) / (1 - share)
+            other = 1 / (1 - share)  # (of a dim with other records only)
+            assert (torch.maximum((left - 1).abs(), (other - 1).abs()) > 2 * rel).any(0).all(), b
