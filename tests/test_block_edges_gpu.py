@@ -216,3 +216,59 @@ def test_every_record_counts(qk, lens, rows, Hkv, G, D):  # noqa: F811
             left = (1 - share / dim[:, torch.arange(R, device="cuda") % D]) / (1 - share)
             other = 1 / (1 - share)  # (of a dim with other records only)
             assert (torch.maximum((left - 1).abs(), (other - 1).abs()) > 2 * rel).any(0).all(), b
+
+
+# ------------------------------------------------------------------------------ other threads and streams
+
+def step_calls(qk):  # noqa: F811
+    """The calls of a step on small inputs, each returning its new outputs."""
+    r = lambda *s: torch.randn(*s, device="cuda").bfloat16()  # noqa: E731
+    x, q, k = r(4, 256), r(4, 8, 64), r(4, 2, 64)
+    pos, table, lens = i32([0, 1, 2, 3]), i32([[0], [1], [2], [3]]), i32([1, 1, 1, 1])
+    cache = torch.zeros(4, 2, 16, 72, dtype=torch.uint8, device="cuda")
+    freq = qk.qk_rope_frequencies(64)
+    out = torch.empty_like(q)
+    ws = torch.empty(qk.qk_kv4_attention_workspace_size(64), dtype=torch.uint8, device="cuda")
+    return {
+        "norm": lambda **o: qk.qk_rmsnorm_quantize(x, None, x, with_xsum=True, **o),
+        "rope": lambda **o: qk.qk_rope(q, k, pos, freq, **o),
+        "append": lambda **o: qk.qk_kv4_append(k, k, cache, table, lens, **o),
+        "gather": lambda **o: qk.qk_kv4_gather(cache, table, lens, None, 4, **o),
+        "attention": lambda **o: qk.qk_kv4_attention(q, cache, table, lens, out=out, workspace=ws, **o),
+    }
+
+
+@pytest.mark.parametrize("name", ["norm", "rope", "append", "gather", "attention"])
+def test_other_threads_run_while_a_call_waits(qk, name):  # noqa: F811
+    """A call that waits for room in the launch queue does not hold the interpreter's lock."""
+    call = step_calls(qk)[name]
+    call()
+    torch.cuda.synchronize()
+    ticks, stop = [], threading.Event()
+
+    def tick():
+        while not stop.is_set():
+            ticks.append(time.perf_counter())
+            time.sleep(0.002)
+
+    t = threading.Thread(target=tick)
+    t.start()
+    try:
+        torch.cuda._sleep(800_000_000)  # 0.4 s and more, behind which the launches pile up
+        longest = (0.0, 0.0, 0.0)
+        for _ in range(4000):
+            a = time.perf_counter()
+            call()
+            b = time.perf_counter()
+            longest = max(longest, (b - a, a, b))
+            if b - a > 0.1:
+                break
+    finally:
+        torch.cuda.synchronize()
+        stop.set()
+        t.join()
+    took, a, b = longest
+    assert took > 0.1, "the queue was never full"
+    inside = [a] + [x for x in ticks if a < x < b] + [b]
+    assert max(y - x for x, y in zip(inside, inside[1:])) < took / 2
+    qk.qk_check_device_error()

@@ -5,7 +5,8 @@
 // outputs and converting twenty ctypes arguments in Python takes 10 to 20.  The
 // same checks, with the same exceptions, and the allocations are made here, and
 // the C calls of include/qk.h with the raw pointers: 3 to 7 us with the launches (2.4 us each).
-// Nothing is computed here.
+// Nothing is computed here.  The C calls and the allocations run without the interpreter's lock, as
+// through ctypes: a launch waits where the queue is full.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -34,6 +35,16 @@ using std::string;
 [[noreturn]] void type_error(const string& s) {
   PyErr_SetString(PyExc_TypeError, s.c_str());
   throw python_error();
+}
+
+// What f does, without the interpreter's lock (taken again when it throws, too).
+template <typename F>
+auto unlocked(F f) {
+  struct Lock {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Lock() { PyEval_RestoreThread(state); }
+  } lock;
+  return f();
 }
 
 string text(at::IntArrayRef v) {
@@ -76,8 +87,10 @@ Tensor output(PyObject* o, at::IntArrayRef shape, ScalarType dtype, const Tensor
       stride[i] = step;
       step *= shape[i] > 1 ? shape[i] : 1;
     }
-    return Tensor(at::detail::empty_strided_cuda(shape, at::IntArrayRef(stride, shape.size()), dtype,
-                                                 beside.device()));
+    return unlocked([&] {
+      return Tensor(at::detail::empty_strided_cuda(shape, at::IntArrayRef(stride, shape.size()), dtype,
+                                                   beside.device()));
+    });
   }
   const Tensor& t = need(o, dtype, (int64_t)shape.size(), name);
   need_shape(t, shape, name);
@@ -114,7 +127,8 @@ class Together {
   void make() {
     if (n_ == 0) return;
     const int64_t one = 1;
-    const at::TensorBase all = at::detail::empty_strided_cuda(bytes_, one, ScalarType::Byte, device_);
+    const at::TensorBase all =
+        unlocked([&] { return at::detail::empty_strided_cuda(bytes_, one, ScalarType::Byte, device_); });
     for (int i = 0; i < n_; ++i) {
       const Part& p = parts_[i];
       auto impl = c10::make_intrusive<at::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
@@ -243,9 +257,12 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (sums || a[7] != Py_None) take(a[7], &xsum, {M, K / 64}, ScalarType::Int, "xsum");
   fresh.make();
   same_device(x, weight, residual, h, xq, sx, xsum);
-  check(qk_rmsnorm_quantize(ptr<uint16_t>(x), ptr<uint16_t>(residual), M, K, ptr<float>(weight),
-                            (float)number(a[3]), ptr<uint16_t>(h), ptr<int8_t>(xq), ptr<float>(sx),
-                            ptr<int32_t>(xsum), stream_of(a[9])),
+  const float eps = (float)number(a[3]);
+  const qk_stream_t stream = stream_of(a[9]);
+  check(unlocked([&] {
+          return qk_rmsnorm_quantize(ptr<uint16_t>(x), ptr<uint16_t>(residual), M, K, ptr<float>(weight), eps,
+                                     ptr<uint16_t>(h), ptr<int8_t>(xq), ptr<float>(sx), ptr<int32_t>(xsum), stream);
+        }),
         "qk_rmsnorm_quantize");
   return tuple_of({hand_back(a[4], h), hand_back(a[5], xq), hand_back(a[6], sx), hand_back(a[7], xsum)});
   END_HANDLE_TH_ERRORS
@@ -287,9 +304,14 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (q_out.size(0) != T || (k.defined() && (k.size(0) != T || k_out.size(0) != T)))
     value_error("q, k and the outputs must have the same number of rows");
   same_device(q, k, positions, freq, q_out, k_out);
-  check(qk_rope(ptr<uint16_t>(q), qs, ptr<uint16_t>(q_out), qos, H, ptr<uint16_t>(k), ks,
-                ptr<uint16_t>(k_out), kos, Hkv, T, D, 2 * freq.size(0), (int)integer(a[4]),
-                ptr<int32_t>(positions), ptr<double>(freq), (float)number(a[5]), stream_of(a[8])),
+  const int layout = (int)integer(a[4]);
+  const float amplitude = (float)number(a[5]);
+  const qk_stream_t stream = stream_of(a[8]);
+  check(unlocked([&] {
+          return qk_rope(ptr<uint16_t>(q), qs, ptr<uint16_t>(q_out), qos, H, ptr<uint16_t>(k), ks,
+                         ptr<uint16_t>(k_out), kos, Hkv, T, D, 2 * freq.size(0), layout, ptr<int32_t>(positions),
+                         ptr<double>(freq), amplitude, stream);
+        }),
         "qk_rope");
   return tuple_of({hand_back(a[6], q_out), hand_back(a[7], k_out)});
   END_HANDLE_TH_ERRORS
@@ -333,9 +355,12 @@ PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t ks = rows(k, c.Hkv, c.D, "k"), vs = rows(v, c.Hkv, c.D, "v");
   if (v.size(0) != T) value_error("k and v must have the same number of rows");
   same_device(k, v, c.cache, c.table, c.lens, c.cu);
-  check(qk_kv4_append(ptr<uint16_t>(k), ks, ptr<uint16_t>(v), vs, T, c.Hkv, c.D, ptr<int32_t>(c.table), c.B,
-                      c.max_pages, ptr<int32_t>(c.lens), ptr<int32_t>(c.cu), ptr<void>(c.cache), c.num_pages,
-                      c.page, stream_of(a[6])),
+  const qk_stream_t stream = stream_of(a[6]);
+  check(unlocked([&] {
+          return qk_kv4_append(ptr<uint16_t>(k), ks, ptr<uint16_t>(v), vs, T, c.Hkv, c.D, ptr<int32_t>(c.table), c.B,
+                               c.max_pages, ptr<int32_t>(c.lens), ptr<int32_t>(c.cu), ptr<void>(c.cache), c.num_pages,
+                               c.page, stream);
+        }),
         "qk_kv4_append");
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
@@ -365,9 +390,12 @@ PyObject* kv4_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
   fresh.make();
   if (k.size(0) != T || v.size(0) != T) value_error("k and v must have " + std::to_string(T) + " rows");
   same_device(k, v, c.cache, c.table, c.lens, c.cu);
-  check(qk_kv4_gather(ptr<void>(c.cache), c.num_pages, c.page, c.Hkv, c.D, ptr<int32_t>(c.table), c.B,
-                      c.max_pages, ptr<int32_t>(c.lens), ptr<int32_t>(c.cu), T, ptr<uint16_t>(k), ks,
-                      ptr<uint16_t>(v), vs, stream_of(a[7])),
+  const qk_stream_t stream = stream_of(a[7]);
+  check(unlocked([&] {
+          return qk_kv4_gather(ptr<void>(c.cache), c.num_pages, c.page, c.Hkv, c.D, ptr<int32_t>(c.table), c.B,
+                               c.max_pages, ptr<int32_t>(c.lens), ptr<int32_t>(c.cu), T, ptr<uint16_t>(k), ks,
+                               ptr<uint16_t>(v), vs, stream);
+        }),
         "qk_kv4_gather");
   return tuple_of({hand_back(a[5], k), hand_back(a[6], v)});
   END_HANDLE_TH_ERRORS
@@ -397,10 +425,12 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const double scale = a[5] == Py_None ? 1.0 / std::sqrt((double)c.D) : number(a[5]);
   same_device(q, out, ws, c.cache, c.table, c.lens, c.cu);
-  check(qk_kv4_attention(ptr<uint16_t>(q), qs, T, H, c.Hkv, c.D, ptr<void>(c.cache), c.num_pages, c.page,
-                         ptr<int32_t>(c.table), c.B, c.max_pages, ptr<int32_t>(c.lens), ptr<int32_t>(c.cu),
-                         (float)scale, integer(a[6]), integer(a[7]), ptr<uint16_t>(out), ptr<void>(ws),
-                         ws_bytes, stream),
+  const int64_t window = integer(a[6]), sinks = integer(a[7]);
+  check(unlocked([&] {
+          return qk_kv4_attention(ptr<uint16_t>(q), qs, T, H, c.Hkv, c.D, ptr<void>(c.cache), c.num_pages, c.page,
+                                  ptr<int32_t>(c.table), c.B, c.max_pages, ptr<int32_t>(c.lens), ptr<int32_t>(c.cu),
+                                  (float)scale, window, sinks, ptr<uint16_t>(out), ptr<void>(ws), ws_bytes, stream);
+        }),
         "qk_kv4_attention");
   return hand_back(a[8], out);
   END_HANDLE_TH_ERRORS
