@@ -272,3 +272,73 @@ def test_other_threads_run_while_a_call_waits(qk, name):  # noqa: F811
     inside = [a] + [x for x in ticks if a < x < b] + [b]
     assert max(y - x for x, y in zip(inside, inside[1:])) < took / 2
     qk.qk_check_device_error()
+
+
+def test_new_outputs_on_another_stream(qk):  # noqa: F811
+    """A call on a stream that is not the current one takes its new outputs from that stream's memory: what the
+    current stream has queued may still read memory that is free to Python."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    M, K, N = 512, 1024, 1024
+    x, w = r(M, K).bfloat16(), r(N, K)
+    q, k = r(M, 8, 64).bfloat16(), r(M, 2, 64).bfloat16()
+    pos = torch.arange(M, dtype=torch.int32, device="cuda")
+    table, lens = torch.arange(32, dtype=torch.int32, device="cuda").view(1, 32), i32([M])
+    cache = torch.zeros(32, 2, 16, 72, dtype=torch.uint8, device="cuda")
+    qk.qk_kv4_append(k, k, cache, table, lens)
+    freq = qk.qk_rope_frequencies(64)
+    W8, s8 = qk.qk_quantize_weights_int8(w)
+    W4, s4, o4 = qk.qk_quantize_weights_int4(w)
+    planes, _ = qk.qk_w4a8_prepare(W4, s4, o4)
+    xq, sx, xsum = qk.qk_quantize_activations(x, with_xsum=True)
+    bias, heads = r(N), r(1, 4, 128, 128).bfloat16()
+    calls = {
+        "weights8": lambda **o: qk.qk_quantize_weights_int8(w, **o),
+        "weights4": lambda **o: qk.qk_quantize_weights_int4(w, **o),
+        "activations": lambda **o: qk.qk_quantize_activations(x, with_xsum=True, **o),
+        "w8a8": lambda **o: qk.qk_w8a8_linear(x, W8, s8, **o),
+        "w8a8 fused": lambda **o: qk.qk_w8a8_linear(x, W8, s8, fused=True, **o),
+        "w8a8 gated": lambda **o: qk.qk_w8a8_linear_gated(x, W8, s8, bias, bias, x, **o),
+        "w8a8 gemm": lambda **o: qk.qk_w8a8_gemm(xq, sx, W8, s8, **o),
+        "w8a8 noalloc": lambda **o: qk.qk_w8a8_linear_noalloc(x, W8, s8, **o),
+        "w4a8": lambda **o: qk.qk_w4a8_linear(x, W4, s4, o4, **o),
+        "w4a8 gemm": lambda **o: qk.qk_w4a8_gemm(xq, sx, xsum, W4, s4, o4, **o),
+        "w4a8 prepare": lambda **o: qk.qk_w4a8_prepare(W4, s4, o4, **o)[0],
+        "w4a8 prepared": lambda **o: qk.qk_w4a8_linear_prepared(x, W4, s4, o4, planes, **o),
+        "w4a8 gemm prepared": lambda **o: qk.qk_w4a8_gemm_prepared(xq, sx, xsum, W4, s4, o4, planes, **o),
+        "sage": lambda **o: qk.qk_sage_attention(heads, heads, heads, **o),
+        "acc8": lambda **o: qk.qk_debug_w8a8_acc(xq, W8, **o),
+        "acc4": lambda **o: qk.qk_debug_w4a8_group_acc(xq, W4, 0, 8, qk.QK_ROUTE_GEMM, **o),
+        "norm": lambda **o: qk.qk_rmsnorm_quantize(x, None, x, with_xsum=True, **o),
+        "frequencies": lambda **o: qk.qk_rope_frequencies(64, **o),
+        "rope": lambda **o: qk.qk_rope(q, k, pos, freq, **o),
+        "gather": lambda **o: qk.qk_kv4_gather(cache, table, lens, None, M, **o),
+        "attention": lambda **o: qk.qk_kv4_attention(q, cache, table, lens, **o),
+    }
+    tensors = lambda out: [t for t in (out if isinstance(out, tuple) else (out,)) if t is not None]  # noqa: E731
+    side = torch.cuda.Stream()
+    for name, call in calls.items():
+        for stream in (side, side.cuda_stream):
+            want = tensors(call())
+            torch.cuda.synchronize()
+            torch.cuda.empty_cache()
+            # memory of the sizes that the call may ask for, free to Python, read by the current stream later
+            storages = {t.untyped_storage().data_ptr(): t.untyped_storage().nbytes() for t in want}
+            side.wait_stream(torch.cuda.current_stream())
+            old = [torch.full((n,), 77, dtype=torch.uint8, device="cuda") for n in storages.values() for _ in range(3)]
+            old += [torch.full((t.nbytes,), 77, dtype=torch.uint8, device="cuda") for t in want]
+            side.wait_stream(torch.cuda.current_stream())
+            torch.cuda._sleep(20_000_000)
+            late = [t.clone() for t in old]
+            spans = [(t.data_ptr(), t.data_ptr() + t.nbytes) for t in old]
+            del old
+            got = tensors(call(stream=stream))
+            for t in got:
+                assert not any(a < t.data_ptr() + t.nbytes and t.data_ptr() < e for a, e in spans), name
+            torch.cuda.synchronize()
+            assert all((t == 77).all() for t in late), name
+            if name != "w4a8 prepare":  # (planes that the weight does not need are not written)
+                assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want)), name
+            del got, late
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    qk.qk_check_device_error()

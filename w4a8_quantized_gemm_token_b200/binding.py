@@ -3,6 +3,9 @@
 Argument marshalling only: each function checks tensor dtypes, devices and
 contiguity, allocates outputs with ``torch.empty`` when the caller passes none,
 and forwards raw device pointers plus the current torch stream to the C call.
+With ``stream=`` (a torch.cuda.Stream or a raw handle) a call runs there; its new
+outputs come from that stream's memory, and as with torch.cuda.stream the caller
+orders the two streams (inputs ready, outputs waited for or record_stream'ed).
 Every step of the computation runs in the library's CUDA kernels; there is no
 CPU fallback.  A non-zero status raises :class:`QKError`.  If the library has
 not been built, importing this module raises.  The calls that a decode step makes
@@ -151,9 +154,20 @@ def _need(t, dtype, ndim, name):
     return t
 
 
-def _out(t, shape, dtype, device, name):
-    if t is None:
+def _new(shape, dtype, device, stream):
+    """A new output, from the memory of the stream that writes it (as under torch.cuda.stream): the
+    current stream's may still be read by what that stream has queued."""
+    if stream is None or _stream(stream) == _stream(None):
         return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out(t, shape, dtype, device, name, stream=None):
+    if t is None:
+        return _new(shape, dtype, device, stream)
     _need(t, dtype, len(shape), name)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -166,8 +180,8 @@ def qk_quantize_weights_int8(W, Wq=None, sw=None, stream=None):
     """W fp32 [N, K] -> (Wq int8 [N, K], sw fp32 [N])."""
     _need(W, torch.float32, 2, "W")
     N, K = W.shape
-    Wq = _out(Wq, (N, K), torch.int8, W.device, "Wq")
-    sw = _out(sw, (N,), torch.float32, W.device, "sw")
+    Wq = _out(Wq, (N, K), torch.int8, W.device, "Wq", stream)
+    sw = _out(sw, (N,), torch.float32, W.device, "sw", stream)
     _check(lib.qk_quantize_weights_int8(_ptr(W), N, K, _ptr(Wq), _ptr(sw), _stream(stream)),
            "qk_quantize_weights_int8")
     return Wq, sw
@@ -177,9 +191,9 @@ def qk_quantize_weights_int4(W, Wp=None, wscale=None, woffset=None, stream=None)
     """W fp32 [N, K] -> (Wp uint8 [N, K/2], wscale fp16 [N, K/64], woffset fp16 [N, K/64])."""
     _need(W, torch.float32, 2, "W")
     N, K = W.shape
-    Wp = _out(Wp, (N, K // 2), torch.uint8, W.device, "Wp")
-    wscale = _out(wscale, (N, K // 64), torch.float16, W.device, "wscale")
-    woffset = _out(woffset, (N, K // 64), torch.float16, W.device, "woffset")
+    Wp = _out(Wp, (N, K // 2), torch.uint8, W.device, "Wp", stream)
+    wscale = _out(wscale, (N, K // 64), torch.float16, W.device, "wscale", stream)
+    woffset = _out(woffset, (N, K // 64), torch.float16, W.device, "woffset", stream)
     _check(lib.qk_quantize_weights_int4(_ptr(W), N, K, _ptr(Wp), _ptr(wscale), _ptr(woffset),
                                         _stream(stream)), "qk_quantize_weights_int4")
     return Wp, wscale, woffset
@@ -189,10 +203,10 @@ def qk_quantize_activations(x, xq=None, sx=None, xsum=None, with_xsum=False, str
     """x bf16 [M, K] -> (xq int8 [M, K], sx fp32 [M], xsum int32 [M, K/64] or None)."""
     _need(x, torch.bfloat16, 2, "x")
     M, K = x.shape
-    xq = _out(xq, (M, K), torch.int8, x.device, "xq")
-    sx = _out(sx, (M,), torch.float32, x.device, "sx")
+    xq = _out(xq, (M, K), torch.int8, x.device, "xq", stream)
+    sx = _out(sx, (M,), torch.float32, x.device, "sx", stream)
     if with_xsum or xsum is not None:
-        xsum = _out(xsum, (M, K // 64), torch.int32, x.device, "xsum")
+        xsum = _out(xsum, (M, K // 64), torch.int32, x.device, "xsum", stream)
     _check(lib.qk_quantize_activations(_ptr(x), M, K, _ptr(xq), _ptr(sx), _ptr(xsum),
                                        _stream(stream)), "qk_quantize_activations")
     return xq, sx, xsum
@@ -208,7 +222,7 @@ def qk_w8a8_linear(x, Wq, sw, bias=None, y=None, workspace=None, stream=None, fu
         _need(bias, torch.float32, 1, "bias")
     M, K = x.shape
     N = Wq.shape[0]
-    y = _out(y, (M, N), torch.bfloat16, x.device, "y")
+    y = _out(y, (M, N), torch.bfloat16, x.device, "y", stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     fn = lib.qk_w8a8_linear_fused if fused else lib.qk_w8a8_linear
     _check(fn(_ptr(x), M, K, _ptr(Wq), _ptr(sw), _ptr(bias), N, _ptr(y), _ptr(workspace),
@@ -230,7 +244,7 @@ def qk_w8a8_linear_gated(x, Wq, sw, bias, gate, residual, y=None, workspace=None
     N = Wq.shape[0]
     if tuple(residual.shape) != (M, N) or gate.shape[0] != N:
         raise ValueError("residual must be [M, N] and gate [N]")
-    y = _out(y, (M, N), torch.bfloat16, x.device, "y")
+    y = _out(y, (M, N), torch.bfloat16, x.device, "y", stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.qk_w8a8_linear_gated(_ptr(x), M, K, _ptr(Wq), _ptr(sw), _ptr(bias), _ptr(gate),
                                     _ptr(residual), N, _ptr(y), _ptr(workspace), ws_bytes,
@@ -247,7 +261,7 @@ def qk_w8a8_gemm(xq, sx, Wq, sw, bias=None, y=None, stream=None):
         _need(bias, torch.float32, 1, "bias")
     M, K = xq.shape
     N = Wq.shape[0]
-    y = _out(y, (M, N), torch.bfloat16, xq.device, "y")
+    y = _out(y, (M, N), torch.bfloat16, xq.device, "y", stream)
     _check(lib.qk_w8a8_gemm(_ptr(xq), _ptr(sx), M, K, _ptr(Wq), _ptr(sw), _ptr(bias), N, _ptr(y),
                             _stream(stream)), "qk_w8a8_gemm")
     return y
@@ -263,7 +277,7 @@ def qk_w8a8_linear_noalloc(x, Wq, sw, bias=None, y=None, stream=None):
         _need(bias, torch.float32, 1, "bias")
     M, K = x.shape
     N = Wq.shape[0]
-    y = _out(y, (M, N), torch.bfloat16, x.device, "y")
+    y = _out(y, (M, N), torch.bfloat16, x.device, "y", stream)
     _check(lib.qk_w8a8_linear_noalloc(_ptr(x), M, K, _ptr(Wq), _ptr(sw), _ptr(bias), N, _ptr(y),
                                       _stream(stream)),
            "qk_w8a8_linear_noalloc")
@@ -279,7 +293,7 @@ def qk_w4a8_linear(x, Wp, wscale, woffset, bias=None, y=None, workspace=None, st
         _need(bias, torch.float32, 1, "bias")
     M, K = x.shape
     N = Wp.shape[0]
-    y = _out(y, (M, N), torch.bfloat16, x.device, "y")
+    y = _out(y, (M, N), torch.bfloat16, x.device, "y", stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.qk_w4a8_linear(_ptr(x), M, K, _ptr(Wp), _ptr(wscale), _ptr(woffset), _ptr(bias),
                               N, _ptr(y), _ptr(workspace), ws_bytes, _stream(stream)),
@@ -301,7 +315,7 @@ def qk_w4a8_prepare(Wp, wscale, woffset, prepared=None, stream=None):
     N, K = Wp.shape[0], Wp.shape[1] * 2
     if prepared is None:
         size = lib.qk_w4a8_prepared_size(N, K)
-        prepared = torch.empty(max(int(size), 1), dtype=torch.uint8, device=Wp.device)
+        prepared = _new(max(int(size), 1), torch.uint8, Wp.device, stream)
     else:
         _need(prepared, torch.uint8, 1, "prepared")
     planes = ctypes.c_int(0)
@@ -322,7 +336,7 @@ def qk_w4a8_linear_prepared(x, Wp, wscale, woffset, prepared, bias=None, y=None,
         _need(bias, torch.float32, 1, "bias")
     M, K = x.shape
     N = Wp.shape[0]
-    y = _out(y, (M, N), torch.bfloat16, x.device, "y")
+    y = _out(y, (M, N), torch.bfloat16, x.device, "y", stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.qk_w4a8_linear_prepared(_ptr(x), M, K, _ptr(Wp), _ptr(wscale), _ptr(woffset),
                                        _ptr(prepared), _ptr(bias), N, _ptr(y), _ptr(workspace),
@@ -344,7 +358,7 @@ def qk_w4a8_gemm_prepared(xq, sx, xsum, Wp, wscale, woffset, prepared, bias=None
         _need(bias, torch.float32, 1, "bias")
     M, K = xq.shape
     N = Wp.shape[0]
-    y = _out(y, (M, N), torch.bfloat16, xq.device, "y")
+    y = _out(y, (M, N), torch.bfloat16, xq.device, "y", stream)
     _check(lib.qk_w4a8_gemm_prepared(_ptr(xq), _ptr(sx), _ptr(xsum), M, K, _ptr(Wp),
                                      _ptr(wscale), _ptr(woffset), _ptr(prepared), _ptr(bias), N,
                                      _ptr(y), _stream(stream)),
@@ -364,7 +378,7 @@ def qk_w4a8_gemm(xq, sx, xsum, Wp, wscale, woffset, bias=None, y=None, route=QK_
         _need(bias, torch.float32, 1, "bias")
     M, K = xq.shape
     N = Wp.shape[0]
-    y = _out(y, (M, N), torch.bfloat16, xq.device, "y")
+    y = _out(y, (M, N), torch.bfloat16, xq.device, "y", stream)
     _check(lib.qk_w4a8_gemm(_ptr(xq), _ptr(sx), _ptr(xsum), M, K, _ptr(Wp), _ptr(wscale),
                             _ptr(woffset), _ptr(bias), N, _ptr(y), int(route), _stream(stream)),
            "qk_w4a8_gemm")
@@ -380,7 +394,7 @@ def qk_debug_w8a8_acc(xq, Wq, acc=None, stream=None):
     _need(Wq, torch.int8, 2, "Wq")
     M, K = xq.shape
     N = Wq.shape[0]
-    acc = _out(acc, (M, N), torch.int32, xq.device, "acc")
+    acc = _out(acc, (M, N), torch.int32, xq.device, "acc", stream)
     _check(lib.qk_debug_w8a8_acc(_ptr(xq), M, K, _ptr(Wq), N, _ptr(acc), _stream(stream)),
            "qk_debug_w8a8_acc")
     return acc
@@ -391,7 +405,7 @@ def qk_debug_w4a8_group_acc(xq, Wp, m0, m1, route, acc=None, stream=None):
     _need(Wp, torch.uint8, 2, "Wp")
     M, K = xq.shape
     N = Wp.shape[0]
-    acc = _out(acc, (m1 - m0, N, K // 64), torch.int32, xq.device, "acc")
+    acc = _out(acc, (m1 - m0, N, K // 64), torch.int32, xq.device, "acc", stream)
     _check(lib.qk_debug_w4a8_group_acc(_ptr(xq), M, K, _ptr(Wp), N, m0, m1, _ptr(acc), int(route),
                                        _stream(stream)), "qk_debug_w4a8_group_acc")
     return acc
@@ -440,7 +454,7 @@ def qk_sage_attention(q, k, v, scale=None, out=None, workspace=None, stream=None
     B, H, L, D = q.shape
     if k.shape != q.shape or v.shape != q.shape:
         raise ValueError("q, k and v must have the same shape [B, H, L, 128]")
-    out = _out(out, (B, H, L, D), torch.bfloat16, q.device, "out")
+    out = _out(out, (B, H, L, D), torch.bfloat16, q.device, "out", stream)
     if scale is None:
         scale = D ** -0.5
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -469,7 +483,7 @@ def qk_rope_frequencies(rot, base=10000.0, scaling=QK_ROPE_PLAIN, factor=1.0, tr
                         fast=32.0, freq=None, stream=None):
     """fp64 [rot / 2]: turns per position of each pair (see include/qk.h for the scalings)."""
     if freq is None:
-        freq = torch.empty(rot // 2, dtype=torch.float64, device="cuda")
+        freq = _new(rot // 2, torch.float64, torch.device("cuda", torch.cuda.current_device()), stream)
     else:
         _need(freq, torch.float64, 1, "freq")
         if freq.shape[0] != rot // 2:

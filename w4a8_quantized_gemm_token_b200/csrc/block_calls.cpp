@@ -12,6 +12,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -79,18 +80,43 @@ void need_shape(const Tensor& t, at::IntArrayRef shape, const char* name) {
     value_error(string(name) + " must have shape " + text(shape) + ", got " + text(t.sizes()));
 }
 
+int64_t integer(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+
+qk_stream_t current_stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
+qk_stream_t stream_of(PyObject* o) {
+  return o == Py_None ? current_stream() : reinterpret_cast<qk_stream_t>((uintptr_t)integer(o));
+}
+
+// New memory for an output, of the pool of the stream that writes it: the current stream's may
+// still be read by what that stream has queued.
+at::TensorBase memory(at::IntArrayRef shape, at::IntArrayRef stride, ScalarType dtype, at::Device device,
+                      qk_stream_t stream) {
+  return unlocked([&] {
+    if (stream == current_stream()) return at::detail::empty_strided_cuda(shape, stride, dtype, device);
+    const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(stream, device.index()));
+    return at::detail::empty_strided_cuda(shape, stride, dtype, device);
+  });
+}
+
 // The tensor given for an output, or a new contiguous one.
-Tensor output(PyObject* o, at::IntArrayRef shape, ScalarType dtype, const Tensor& beside, const char* name) {
+Tensor output(PyObject* o, at::IntArrayRef shape, ScalarType dtype, const Tensor& beside, const char* name,
+              qk_stream_t stream) {
   if (o == Py_None) {
     int64_t stride[4], step = 1;
     for (size_t i = shape.size(); i-- > 0;) {
       stride[i] = step;
       step *= shape[i] > 1 ? shape[i] : 1;
     }
-    return unlocked([&] {
-      return Tensor(at::detail::empty_strided_cuda(shape, at::IntArrayRef(stride, shape.size()), dtype,
-                                                   beside.device()));
-    });
+    return Tensor(memory(shape, at::IntArrayRef(stride, shape.size()), dtype, beside.device(), stream));
   }
   const Tensor& t = need(o, dtype, (int64_t)shape.size(), name);
   need_shape(t, shape, name);
@@ -115,7 +141,7 @@ int64_t rows(const Tensor& t, int64_t heads, int64_t D, const char* name) {
 // release take 0.8 us, a tensor beside another one 0.15.
 class Together {
  public:
-  explicit Together(const Tensor& beside) : device_(beside.device()) {}
+  Together(const Tensor& beside, qk_stream_t stream) : device_(beside.device()), stream_(stream) {}
   void add(Tensor* out, std::initializer_list<int64_t> shape, ScalarType dtype) {
     Part& p = parts_[n_++];
     p = {out, {}, (int)shape.size(), dtype, bytes_};
@@ -127,8 +153,7 @@ class Together {
   void make() {
     if (n_ == 0) return;
     const int64_t one = 1;
-    const at::TensorBase all =
-        unlocked([&] { return at::detail::empty_strided_cuda(bytes_, one, ScalarType::Byte, device_); });
+    const at::TensorBase all = memory(bytes_, one, ScalarType::Byte, device_, stream_);
     for (int i = 0; i < n_; ++i) {
       const Part& p = parts_[i];
       auto impl = c10::make_intrusive<at::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
@@ -151,6 +176,7 @@ class Together {
   int n_ = 0;
   int64_t bytes_ = 0;
   at::Device device_;
+  qk_stream_t stream_;
 };
 
 const Tensor& rows_of_three(PyObject* o, const char* name, const char* shape) {
@@ -174,22 +200,6 @@ void same_device(const T&... t) {
 template <typename P>
 P* ptr(const Tensor& t) {
   return t.defined() ? static_cast<P*>(t.data_ptr()) : nullptr;
-}
-
-int64_t integer(PyObject* o) {
-  const long long v = PyLong_AsLongLong(o);
-  if (v == -1 && PyErr_Occurred()) throw python_error();
-  return v;
-}
-double number(PyObject* o) {
-  const double v = PyFloat_AsDouble(o);
-  if (v == -1.0 && PyErr_Occurred()) throw python_error();
-  return v;
-}
-
-qk_stream_t current_stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
-qk_stream_t stream_of(PyObject* o) {
-  return o == Py_None ? current_stream() : reinterpret_cast<qk_stream_t>((uintptr_t)integer(o));
 }
 
 void check(qk_status st, const char* where) {
@@ -230,6 +240,7 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   count(n, 10);
   const Tensor& x = need(a[0], ScalarType::BFloat16, 2, "x");
   const int64_t M = x.size(0), K = x.size(1);
+  const qk_stream_t stream = stream_of(a[9]);
   Tensor weight, residual, h, xsum;
   if (a[1] != Py_None) {
     weight = need(a[1], ScalarType::Float, 1, "weight");
@@ -238,19 +249,19 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (a[2] != Py_None) {
     residual = need(a[2], ScalarType::BFloat16, 2, "residual");
     if (residual.sizes() != x.sizes()) value_error("residual must have x's shape");
-    h = output(a[4], {M, K}, ScalarType::BFloat16, x, "h");
+    h = output(a[4], {M, K}, ScalarType::BFloat16, x, "h", stream);
   } else if (a[4] != Py_None) {
     value_error("h is written with a residual only");
   }
   const int sums = PyObject_IsTrue(a[8]);
   if (sums < 0) throw python_error();
   Tensor xq, sx;  // (used and released together, and with the sums)
-  Together fresh(x);
+  Together fresh(x, stream);
   auto take = [&](PyObject* o, Tensor* t, std::initializer_list<int64_t> shape, ScalarType dtype, const char* name) {
     if (o == Py_None)
       fresh.add(t, shape, dtype);
     else
-      *t = output(o, shape, dtype, x, name);
+      *t = output(o, shape, dtype, x, name, stream);
   };
   take(a[5], &xq, {M, K}, ScalarType::Char, "xq");
   take(a[6], &sx, {M}, ScalarType::Float, "sx");
@@ -258,7 +269,6 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   fresh.make();
   same_device(x, weight, residual, h, xq, sx, xsum);
   const float eps = (float)number(a[3]);
-  const qk_stream_t stream = stream_of(a[9]);
   check(unlocked([&] {
           return qk_rmsnorm_quantize(ptr<uint16_t>(x), ptr<uint16_t>(residual), M, K, ptr<float>(weight), eps,
                                      ptr<uint16_t>(h), ptr<int8_t>(xq), ptr<float>(sx), ptr<int32_t>(xsum), stream);
@@ -278,8 +288,9 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& positions = need(a[2], ScalarType::Int, 1, "positions");
   const Tensor& freq = need(a[3], ScalarType::Double, 1, "freq");
   if (positions.size(0) != T) value_error("positions must have shape [" + std::to_string(T) + "]");
+  const qk_stream_t stream = stream_of(a[8]);
   Tensor k, q_out, k_out;
-  Together fresh(q);
+  Together fresh(q, stream);
   auto out = [&](PyObject* o, Tensor* t, const Tensor& like, const char* name, int64_t* stride) {
     const int64_t heads = like.size(1);
     *stride = heads * D;
@@ -306,7 +317,6 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   same_device(q, k, positions, freq, q_out, k_out);
   const int layout = (int)integer(a[4]);
   const float amplitude = (float)number(a[5]);
-  const qk_stream_t stream = stream_of(a[8]);
   check(unlocked([&] {
           return qk_rope(ptr<uint16_t>(q), qs, ptr<uint16_t>(q_out), qos, H, ptr<uint16_t>(k), ks,
                          ptr<uint16_t>(k_out), kos, Hkv, T, D, 2 * freq.size(0), layout, ptr<int32_t>(positions),
@@ -373,7 +383,8 @@ PyObject* kv4_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t T = integer(a[4]);
   if (T < 0) value_error("T must not be negative");
   const Cache c(a[0], a[1], a[2], a[3], T);
-  Together fresh(c.cache);
+  const qk_stream_t stream = stream_of(a[7]);
+  Together fresh(c.cache, stream);
   auto out = [&](PyObject* o, Tensor* t, const char* name, int64_t* stride) {
     *stride = c.Hkv * c.D;
     if (o == Py_None) {
@@ -390,7 +401,6 @@ PyObject* kv4_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
   fresh.make();
   if (k.size(0) != T || v.size(0) != T) value_error("k and v must have " + std::to_string(T) + " rows");
   same_device(k, v, c.cache, c.table, c.lens, c.cu);
-  const qk_stream_t stream = stream_of(a[7]);
   check(unlocked([&] {
           return qk_kv4_gather(ptr<void>(c.cache), c.num_pages, c.page, c.Hkv, c.D, ptr<int32_t>(c.table), c.B,
                                c.max_pages, ptr<int32_t>(c.lens), ptr<int32_t>(c.cu), T, ptr<uint16_t>(k), ks,
@@ -409,8 +419,8 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t T = q.size(0), H = q.size(1);
   const Cache c(a[1], a[2], a[3], a[4], T);
   const int64_t qs = rows(q, H, c.D, "q");
-  const Tensor out = output(a[8], {T, H, c.D}, ScalarType::BFloat16, q, "out");
   const qk_stream_t stream = stream_of(a[10]);
+  const Tensor out = output(a[8], {T, H, c.D}, ScalarType::BFloat16, q, "out", stream);
   // without a workspace: torch's allocator on the current stream; on another one the
   // library allocates in that stream's order
   Tensor ws;
@@ -421,7 +431,7 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     ws_bytes = ws.nbytes();
   } else if (a[10] == Py_None || stream == current_stream()) {
     ws_bytes = qk_kv4_attention_workspace_size(c.D);
-    ws = output(Py_None, {(int64_t)ws_bytes}, ScalarType::Byte, q, "workspace");
+    ws = output(Py_None, {(int64_t)ws_bytes}, ScalarType::Byte, q, "workspace", stream);
   }
   const double scale = a[5] == Py_None ? 1.0 / std::sqrt((double)c.D) : number(a[5]);
   same_device(q, out, ws, c.cache, c.table, c.lens, c.cu);
