@@ -26,7 +26,23 @@ if not os.path.exists(_LIB_PATH):
         "(the quantized linear has no CPU fallback)")
 
 lib = ctypes.CDLL(_LIB_PATH)
-from . import _block_calls  # noqa: E402  (built beside libqk.so, and linked to it)
+
+
+class _NotLoaded:
+    """In the place of _block_calls: says why at the first call that needs it."""
+
+    def __init__(self, why):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"_block_calls (for {name}) cannot be loaded: {self.why}.  Rebuild it: "
+                          "python -m w4a8_quantized_gemm_token_b200.build")
+
+
+try:  # built beside libqk.so and linked to it, for one Python and one torch; the linears do without
+    from . import _block_calls
+except ImportError as _e:
+    _block_calls = _NotLoaded(_e)
 
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _F, _D = ctypes.c_float, ctypes.c_double

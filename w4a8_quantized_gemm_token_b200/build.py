@@ -1,5 +1,6 @@
 """Build libqk.so (the CUDA library behind include/qk.h) in-tree with nvcc, and
-_block_calls.so (csrc/block_calls.cpp, calls of it for binding.py) with g++.
+_block_calls (csrc/block_calls.cpp, calls of it for binding.py) with g++, for this
+Python and this torch.
 
 Every .cu under csrc/ is compiled for sm_100a only
 (``-gencode arch=compute_100a,code=sm_100a``), objects go to ``_build/``, and
@@ -11,6 +12,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -24,7 +26,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqk.so")
-CALLS = os.path.join(PKG, "_block_calls.so")
+CALLS = os.path.join(PKG, "_block_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
+CALLS_ABI = os.path.join(BUILD, "block_calls.abi")  # what CALLS was built against
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -79,9 +82,14 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
 
 def _build_calls(verbose: bool) -> None:
     src = os.path.join(CSRC, "block_calls.cpp")
-    if not _newer(CALLS, [src, os.path.join(INCLUDE, "qk.h")]):
-        return
     torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    abi = f"Python {sys.version}\ntorch {importlib.metadata.version('torch')} in {torch_dir}\n"
+    built = None
+    if os.path.exists(CALLS_ABI):
+        with open(CALLS_ABI) as f:
+            built = f.read()
+    if built == abi and not _newer(CALLS, [src, os.path.join(INCLUDE, "qk.h")]):
+        return
     inc = os.path.join(torch_dir, "include")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     tmp = CALLS + f".tmp{os.getpid()}"
@@ -96,8 +104,10 @@ def _build_calls(verbose: bool) -> None:
     if verbose or r.returncode != 0:
         sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
     if r.returncode != 0:
-        raise RuntimeError("g++ failed building _block_calls.so")
+        raise RuntimeError("g++ failed building _block_calls")
     os.replace(tmp, CALLS)
+    with open(CALLS_ABI, "w") as f:
+        f.write(abi)
 
 
 if __name__ == "__main__":
