@@ -63,3 +63,49 @@ def test_the_block_calls_are_built_for_this_python_and_torch(monkeypatch, tmp_pa
     (tmp_path / "calls.abi").unlink()
     build._build_calls(False)
     assert len(runs) == 4
+
+
+PTXAS = """ptxas info    : 0 bytes gmem
+ptxas info    : Compiling entry function '_ZN2qk63_GLOBAL__N__1_12_kv4_chunk_cu_1_221kv4_chunk_join_kernelILi64EEEvNS_7Kv4ArgsE' for 'sm_100a'
+ptxas info    : Used 40 registers, used 1 barriers
+ptxas info    : Compiling entry function '_ZN2qk63_GLOBAL__N__1_12_kv4_chunk_cu_1_216kv4_chunk_kernelILi64EEEvNS_7Kv4ArgsE' for 'sm_100a'
+    8 bytes stack frame, 8 bytes spill stores, 8 bytes spill loads
+ptxas info    : Used {} registers, used 2 barriers
+ptxas info    : Compiling entry function '_ZN2qk63_GLOBAL__N__1_12_kv4_chunk_cu_1_216kv4_chunk_kernelILi128EEEvNS_7Kv4ArgsE' for 'sm_100a'
+ptxas info    : Used {} registers, used 2 barriers
+"""
+
+
+def test_register_splits_are_checked_by_the_build(monkeypatch, tmp_path):
+    """A compiler that chose another number of registers than a kernel's split is of fails the build, and not
+    the first call that is large enough for that kernel."""
+    assert build.launch_registers(PTXAS.format(128, 120), "kv4_chunk_kernel") == [128, 120]
+    assert build.launch_registers(PTXAS.format(128, 120), "kv4_chunk_join_kernel") == [40]
+    src = os.path.join(build.CSRC, "kv4_chunk.cu")
+    assert build.check_split(src, PTXAS.format(128, 128)) == ""
+    for bad in (PTXAS.format(128, 120), PTXAS.format(136, 128), ""):
+        assert "kv4_chunk_kernel" in build.check_split(src, bad)
+    # in the build: the object is not kept
+    real = subprocess.run
+
+    def run(cmd, **kw):
+        if "-c" not in cmd:
+            return real(["true"])
+        with open(cmd[cmd.index("-o") + 1], "w"):
+            pass
+        return subprocess.CompletedProcess(cmd, 0, "", PTXAS.format(128, 120) if "-v" in cmd else "")
+
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build.subprocess, "run", run)
+    with pytest.raises(RuntimeError):
+        build.build()
+    left = os.listdir(tmp_path)
+    assert "kv4_cache.o" in left and not [s for s in build.SPLITS if s[:-3] + ".o" in left]
+
+
+def test_every_split_kernel_is_in_the_list():
+    for name in os.listdir(build.CSRC):
+        if name.endswith(".cu"):
+            with open(os.path.join(build.CSRC, name)) as f:
+                text = f.read()
+            assert ("regs_inc<" in text) == (name in build.SPLITS), name

@@ -15,6 +15,7 @@ import glob
 import importlib.metadata
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -32,6 +33,34 @@ CALLS_ABI = os.path.join(BUILD, "block_calls.abi")  # what CALLS was built again
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC, *ARCH]
+
+# Kernels that share out the registers they are launched with (setmaxnreg): their sources' kRegsLaunch is
+# what the split adds up to, and a launch with another count is refused, so the compiler has to have chosen it.
+SPLITS = {"sage_attn.cu": "sage_attn_kernel", "gemm_w4a8.cu": "w4a8_gemm_kernel", "kv4_chunk.cu": "kv4_chunk_kernel"}
+
+
+def launch_registers(ptxas: str, kernel: str) -> list:
+    """The registers per thread of each instance of the kernel, from what ptxas -v printed."""
+    name = re.compile(rf"Compiling entry function '\S*{len(kernel)}{kernel}[IE]\S*'")
+    counts, mine = [], False
+    for line in ptxas.splitlines():
+        if "Compiling entry function" in line:
+            mine = name.search(line) is not None
+        used = re.search(r"Used (\d+) registers", line)
+        if used and mine:
+            counts.append(int(used.group(1)))
+    return counts
+
+
+def check_split(src: str, ptxas: str) -> str:
+    """What is wrong with the registers of the source's kernel, or nothing."""
+    kernel = SPLITS[os.path.basename(src)]
+    with open(src) as f:
+        want = int(re.search(r"constexpr int kRegsLaunch = (\d+);", f.read()).group(1))
+    counts = launch_registers(ptxas, kernel)
+    if not counts or set(counts) != {want}:
+        return f"{kernel}: compiled to {counts} registers per thread, its split is of {want}\n"
+    return ""
 
 
 def nvcc() -> str:
@@ -60,16 +89,21 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         objs.append(obj)
         if _newer(obj, [src, *headers]) or ptxas_verbose:
             cmd = [nvcc(), *NVCC_FLAGS, "-c", src, "-o", obj]
-            if ptxas_verbose:
+            if ptxas_verbose or os.path.basename(src) in SPLITS:
                 cmd += ["-Xptxas", "-v"]
-            jobs.append(cmd)
+            jobs.append((cmd, src, obj))
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
-        results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
+        results = list(ex.map(lambda c: subprocess.run(c[0], capture_output=True, text=True), jobs))
     failed = False
-    for cmd, r in zip(jobs, results):
-        if verbose or ptxas_verbose or r.returncode != 0:
-            sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-        failed |= r.returncode != 0
+    for (cmd, src, obj), r in zip(jobs, results):
+        wrong = ""
+        if r.returncode == 0 and os.path.basename(src) in SPLITS:
+            wrong = check_split(src, r.stdout + r.stderr)
+            if wrong:
+                os.remove(obj)
+        if verbose or ptxas_verbose or r.returncode != 0 or wrong:
+            sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr + wrong)
+        failed |= r.returncode != 0 or wrong != ""
     if failed:
         raise RuntimeError("nvcc failed building libqk.so")
     if _newer(LIB, objs):

@@ -53,9 +53,11 @@ constexpr int kRows = 128;             // of an item: lanes of tensor memory
 constexpr int kKeys = 64, kLog = 6;    // of a block of keys
 constexpr int kPad = 8;                // what a new item counts for beside its blocks (5, 8, 12: 147, 131, 134 us)
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-// registers a thread: of 128 at launch, for the unpacking, the issuing and two softmax groups
+// registers a thread: of kRegsLaunch at launch (the build checks it), for the unpacking, the issuing and
+// two softmax groups
+constexpr int kRegsLaunch = 128;
 constexpr int kRegsUnpack = 96, kRegsIssue = 48, kRegsSoft = 184;
-static_assert(kRegsUnpack + kRegsIssue + 2 * kRegsSoft <= 4 * 128, "register split");
+static_assert(kRegsUnpack + kRegsIssue + 2 * kRegsSoft <= 4 * kRegsLaunch, "register split");
 
 template <int D>
 struct Cfg {
@@ -998,7 +1000,7 @@ cudaError_t launch(const Kv4Args& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     cudaFuncAttributes fa;  // the register split is of what the block is launched with
     if ((e = cudaFuncGetAttributes(&fa, kv4_chunk_kernel<D>)) != cudaSuccess) return e;
-    if (fa.numRegs != 128) return cudaErrorInvalidKernelImage;
+    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
     done[dev] = true;
   }
   cudaLaunchAttribute attr[1];
