@@ -464,6 +464,9 @@ qk_status qk_sage_attention(const uint16_t *q, const uint16_t *k, const uint16_t
  *   sx   = fl32(fl32(U / 127) rstd);  an all-zero u gets sx = 1, codes 0;
  *          a row with a NaN among its u gets sx = NaN, codes 0
  *   xsum[m, g] = sum of the codes of group g of 64, when xsum is not NULL
+ * (The multiplier is rounded twice, the activation quantization's 127 / absmax once: without
+ * residual and weight the codes are qk_quantize_activations's but where u 127 / U is within
+ * 2^-15 of halfway between two codes; there they may be one apart.)
  * so that xq sx is the norm h rstd weight in 8 bits.  The row's rstd cancels in
  * the codes, which are exact: only sx depends on the fp32 sum of squares.
  *   x        : bf16 bits [M, K]  (in)

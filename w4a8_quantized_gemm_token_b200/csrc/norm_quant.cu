@@ -12,7 +12,7 @@
 // The row's 1 / rms multiplies every element alike, so it cancels in the codes
 // (|u| / U has no rms in it) and goes into the scale: one pass over the row
 // decides every code from u, as act_quant.cuh does from x (with the multiplier from
-// the reciprocal), and no rounding of the sum of squares can move a code.  code sx
+// the reciprocal: below), and no rounding of the sum of squares can move a code.  code sx
 // is the quantized h rstd w.
 //
 // Bound: HBM.  2 (x) + 2 (residual) + 2 (h) + 1 (codes) bytes per element, each
@@ -88,6 +88,9 @@ __device__ __forceinline__ uint2 code_chunk(const float (&u)[8], float r, int* s
   return make_uint2(out[0], out[1]);
 }
 
+// Two roundings (the header's rule), where act_multiplier has one.  Either is within 2^-23 of
+// 127 / U, and a code within 1/2 + 2^-15 of u 127 / U: the two rules' codes differ, by one, only
+// for values that close to halfway between two codes.
 __device__ __forceinline__ float norm_multiplier(float top) {
   return top == 0.0f ? 0.0f : __fmul_rn(127.0f, __fdiv_rn(1.0f, top));
 }
