@@ -342,3 +342,21 @@ def test_new_outputs_on_another_stream(qk):  # noqa: F811
             del got, late
     assert torch.cuda.current_stream() == torch.cuda.default_stream()
     qk.qk_check_device_error()
+
+
+# --------------------------------------------------------------------------------------- one row, none
+
+def test_an_empty_batch(qk):  # noqa: F811
+    """No requests and no rows, with and without row bounds: nothing to do, and no refusal."""
+    cache = torch.zeros(4, 2, 16, 72, dtype=torch.uint8, device="cuda")
+    table = torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    lens = torch.empty(0, dtype=torch.int32, device="cuda")
+    k, q = (torch.empty(0, h, 64, dtype=torch.bfloat16, device="cuda") for h in (2, 8))
+    for cu in (None, i32([0])):
+        qk.qk_kv4_append(k, k, cache, table, lens, cu)
+        assert qk.qk_kv4_attention(q, cache, table, lens, cu).shape == (0, 8, 64)
+        assert [t.shape for t in qk.qk_kv4_gather(cache, table, lens, cu, 0)] == [(0, 2, 64)] * 2
+    with pytest.raises(ValueError):  # rows of no request
+        qk.qk_kv4_attention(torch.zeros(3, 8, 64, dtype=torch.bfloat16, device="cuda"), cache, table, lens)
+    assert not cache.any()
+    qk.qk_check_device_error()

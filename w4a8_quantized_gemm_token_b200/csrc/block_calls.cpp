@@ -348,7 +348,7 @@ struct Cache {
     if (rows != Py_None) {
       cu = need(rows, ScalarType::Int, 1, "cu_rows");
       if (cu.size(0) != B + 1) value_error("cu_rows must have shape [" + std::to_string(B + 1) + "]");
-    } else if (B == 0 || T % B != 0) {
+    } else if (B == 0 ? T != 0 : T % B != 0) {
       value_error("without cu_rows every request has the same number of rows");
     }
   }
