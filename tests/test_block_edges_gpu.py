@@ -360,3 +360,26 @@ def test_an_empty_batch(qk):  # noqa: F811
         qk.qk_kv4_attention(torch.zeros(3, 8, 64, dtype=torch.bfloat16, device="cuda"), cache, table, lens)
     assert not cache.any()
     qk.qk_check_device_error()
+
+
+@pytest.mark.parametrize("wide", [4, 2052, -3])
+def test_the_stride_of_one_row(qk, wide):  # noqa: F811
+    """A single row's distance to the next one means nothing, whatever its view says."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    odd = lambda t: t.as_strided(t.shape, (t.shape[1] * 64 + wide if wide > 0 else 5, 64, 1))  # noqa: E731
+    q, k, v = r(1, 8, 64), r(1, 2, 64), r(1, 2, 64)
+    pos, freq, table, lens = i32([7]), qk.qk_rope_frequencies(64), i32([[1]]), i32([1])
+    caches = [torch.zeros(2, 2, 16, 72, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    want, got = [], []
+    for view, cache, out in ((lambda t: t, caches[0], want), (odd, caches[1], got)):
+        a, b = qk.qk_rope(view(q), view(k), pos, freq)
+        qk.qk_kv4_append(view(b), view(v), cache, table, lens)
+        out += [a, b, qk.qk_kv4_attention(view(a), cache, table, lens)]
+        into = torch.empty_like(k), torch.empty_like(k)
+        qk.qk_kv4_gather(cache, table, lens, None, 1, k=view(into[0]), v=view(into[1]))
+        here = q.clone()
+        qk.qk_rope(view(here), None, pos, freq, q_out=view(here))
+        out += [*into, here]
+    assert all(torch.equal(bits(x), bits(y)) for x, y in zip(want, got)) and torch.equal(*caches)
+    qk.qk_check_device_error()

@@ -134,7 +134,7 @@ int64_t rows(const Tensor& t, int64_t heads, int64_t D, const char* name) {
   if (t.size(0) == 0) return heads * D;
   if ((D > 1 && t.stride(2) != 1) || (heads > 1 && t.stride(1) != D))
     value_error(string(name) + ": a row's heads must be contiguous");
-  return t.size(0) > 1 ? t.stride(0) : std::max(heads * D, t.stride(0));
+  return t.size(0) > 1 ? t.stride(0) : heads * D;  // (of a single row any stride)
 }
 
 // New contiguous tensors in one allocation, 256 bytes apart: an allocation and its
