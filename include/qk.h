@@ -637,8 +637,11 @@ size_t qk_kv4_attention_workspace_size(int64_t D);
  * may be freed.  (H / Hkv) T <= 2^30.
  * Kernels: the attention (one block per SM, equal spans of the cache to its warps,
  * or, for many rows per request, to the block: tiles of 128 rows by tcgen05, with the
- * same precision) and the join of what was cut between blocks.  Which of the two is
- * decided by T, B and the heads alone.
+ * same precision) and the join of what was cut between blocks.  Which of the two, and how
+ * many rows are worked on together, is decided for the whole call from T, B and the heads alone,
+ * by the average T / B (rows of nobody included).  So give requests of very different
+ * numbers of rows calls of their own: a prompt of 2048 rows beside 31 requests of one row over
+ * 8192 tokens (8 kv heads of 4) takes 389 us, in two calls 182.
  */
 qk_status qk_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t T, int64_t H, int64_t Hkv,
                            int64_t D, const void *cache, int64_t num_pages, int64_t page,

@@ -1,7 +1,7 @@
 // block_calls.cpp -- the marshalling of the calls that a decode step makes between its
 // products (norm, rotary positions, the 4-bit cache), for binding.py.
 //
-// Such a call's kernels take 2 to 5 us; checking a dozen tensors, allocating the
+// Such a call's kernels take 2 to 10 us; checking a dozen tensors, allocating the
 // outputs and converting twenty ctypes arguments in Python takes 10 to 20.  The
 // same checks, with the same exceptions, and the allocations are made here, and
 // the C calls of include/qk.h with the raw pointers: 3 to 7 us with the launches (2.4 us each).

@@ -25,9 +25,9 @@
 //
 // Bound: HBM (9 D / 8 bytes per visible token and kv head) and, about as much, the issue
 // of instructions: 239 per record of 16 tokens (D = 128), 83 of them the unpacking.  64
-// requests of 16384 tokens, 8 kv heads: 1.21 GB in 201 us (92 % of the copy rate) at 1965
+// requests of 16384 tokens, 8 kv heads: 1.21 GB in 203 us (91 % of the copy rate) at 1965
 // MHz; in a stream of seconds the power limit takes the clock to about 1650 MHz, and the
-// kernel follows it (240 us).  Few records are bound by latency: 9 us for one
+// kernel follows it (244 us).  Few records are bound by latency: 9.7 us for one
 // request of 500 tokens, most of it the loads that depend on one another (lengths,
 // page, record; metas, pieces).
 // mma.sync is used rather than tcgen05 because its operands are registers: a
@@ -70,7 +70,8 @@ namespace {
 template <int D, int NT>
 struct Cfg {
   static constexpr int ROWS = 8 * NT;
-  // Warps; the registers of the SM over four quarters.  D = 128: 12 of 168 registers (15 of
+  // Warps; the registers of the SM over four quarters.  (Times of each choice and its neighbours
+  // as they were when it was made, not the present ones.)  D = 128: 12 of 168 registers (15 of
   // 128 spill a little: 236 us against 231 for 11 of 168, 64 x 16384), with two tiles 8 of
   // 255 (11 of 168 spill: 70 us against 62, 200 rows over 2500 tokens).  D = 64: 16
   // of 122 (12: 42.4 us against 40.5, 32 requests of 16384), with two tiles 8 of 207 (12
@@ -979,10 +980,13 @@ cudaError_t launch(const Kv4Args& a, cudaStream_t s) {
 
 // Whether kv4_chunk.cu's tiles of 128 rows are the faster ones: where the batch's average
 // request fills three quarters of one per kv head, and there are tiles for most of the SMs.
-// 128 rows a request over 2400 keys, 16 kv heads of 128: 8 requests 67 us (104 here), 4 (64
-// tiles) 42 (59), but over 600 keys 30 (27); 96 rows, 8 requests: 64 (82); 64 rows: 63 (61).
-// 300 rows, 8 kv heads, 4 requests (96 tiles): 54 us over 2400 keys (67), 31 over 600 (28).
-// A prompt of 2048 tokens, 8 kv heads of 4 query heads: 125 us (450).
+// 128 rows a request over 2400 keys, 16 kv heads of 128: 8 requests 68 us (104 here), 4 (64
+// tiles) 43 (59), but over 600 keys 30 (27); 96 rows, 8 requests: 65 (82); 64 rows: 64 (62).
+// 300 rows, 8 kv heads, 4 requests (96 tiles): 55 us over 2400 keys (66), 31 over 600 (29).
+// A prompt of 2048 tokens, 8 kv heads of 4 query heads: 124 us (466).
+// The host knows T and B only, so the average counts the rows of nobody, and one long request
+// decides for all: a prompt of 2048 beside 31 requests of one row over 8192 tokens takes 389 us,
+// in two calls 123 + 59; beside 63 of two query heads per kv head 525, in two calls 69 + 106.
 bool by_chunks(int64_t T, int64_t B, int64_t H, int64_t Hkv) {
   const int64_t rows = H / Hkv * ((T + B - 1) / B);
   return rows >= 96 && B * Hkv * ((rows + 127) / 128) >= 96;
@@ -1018,9 +1022,10 @@ cudaError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t H,
   a.ws = static_cast<uint8_t*>(workspace);
   a.err = err;
   // Rows of an item: 8 where the batch's average request has no more per kv head, else 16.
-  // 16 requests of 8192 tokens, 4 kv heads of 128: with 8 rows 24.8 us (16 to an item: 33.1),
-  // with 9 33.4 (8 to an item, twice the cache: 40.7), with 16 34.9 (40.9).  Of long
-  // chunks of rows both take the same (200 rows over 2500 tokens: 56.8, 59.4).
+  // 16 requests of 8192 tokens, 4 kv heads of 128: with 8 rows 24.9 us (16 to an item: 31.5),
+  // with 9 31.6 (8 to an item, twice the cache: 41.0), with 16 31.8 (41.0).  A chunk of 200 rows
+  // over 2500 tokens, 16 kv heads: 33.4 (36.2).  (One row more than requests is an average of 2:
+  // with 8 query heads per kv head 31.5 us instead of 24.5.)
   const int64_t rows = a.G * ((req.T + req.B - 1) / req.B);
   const bool wide = rows > 8;
   if (by_chunks(req.T, req.B, H, cache.Hkv)) return launch_kv4_chunk(a, s);

@@ -29,13 +29,16 @@
 // from the workspace, in the order of the keys, by kv4_chunk_join_kernel.  A new item costs a
 // block about as much as 8 blocks of keys (queries, a first reference, the join of the two
 // groups), and counts for that in the spans: without it a prompt's short first tiles, one
-// after the other, took 410 us (2048 rows, 8 kv heads, 4 heads each) instead of 125.
+// after the other, took 410 us (2048 rows, 8 kv heads, 4 heads each) instead of 124.
 //
 // Bound: what the softmax groups issue and wait for.  148 items of 128 rows: 25.2 us over 512
-// keys, and 1.15 us for every further 64 (a product of that size is 0.27 us at the tensor
-// cores' rate; D = 64: 0.8 us).  Code that runs once an item is as dear as the code of eight
-// blocks, mostly its instructions' fetch.  What kv4_attn.cu takes for the same: 47.8 us, and
+// keys, and 1.2 us for every further 64 (a product of that size is 0.27 us at the tensor
+// cores' rate; D = 64: 19.5 and 0.85 us).  Code that runs once an item is as dear as the code of eight
+// blocks, mostly its instructions' fetch.  What kv4_attn.cu takes for the same: 47.4 us, and
 // 2.6 us for every further 64 keys.
+// Registers are short on both sides of the split: a thread spills 592 bytes of stores and 500 of
+// loads (D = 64: 380 and 332), partly where the issuing and copying warps walk the items in 48
+// registers.  Local memory takes 1.2 % of the instructions of 32 blocks of keys an item.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -51,7 +54,9 @@ namespace {
 
 constexpr int kRows = 128;             // of an item: lanes of tensor memory
 constexpr int kKeys = 64, kLog = 6;    // of a block of keys
-constexpr int kPad = 8;                // what a new item counts for beside its blocks (5, 8, 12: 147, 131, 134 us)
+// what a new item counts for beside its blocks (5, 8, 12: 147, 131, 134 us for a prompt of 2048 rows, 8 kv
+// heads of 4, when a block of keys still took longer)
+constexpr int kPad = 8;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 // registers a thread: of kRegsLaunch at launch (the build checks it), for the unpacking, the issuing and
 // two softmax groups
@@ -233,7 +238,7 @@ __device__ __forceinline__ float* piece_at(uint8_t* ws, int D, int block, int wh
 }
 
 // Scales and offsets of a pair of keys.  (fp32 in shared memory: as fp16, half the loads and
-// two conversions for each of them, a block of 64 keys took 1.24 us instead of 1.15.)
+// two conversions for each of them, a block of 64 keys took a twelfth longer.)
 template <int NG>
 __device__ __forceinline__ void scales(uint32_t at, uint64_t (&sc)[NG], uint64_t (&of)[NG]) {
 #pragma unroll

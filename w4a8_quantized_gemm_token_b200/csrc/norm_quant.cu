@@ -17,8 +17,9 @@
 //
 // Bound: HBM.  2 (x) + 2 (residual) + 2 (h) + 1 (codes) bytes per element, each
 // touched once: u stays in fp32 registers between the maximum and the codes.
-// 16384 rows of 4096: 75.7 us, 95 % of the copy rate; 1111 rows of 5120: 9.7 us (62 %:
-// one wave of blocks, a load, a reduction and a store long); one row 2.4 us.
+// 16384 rows of 4096: 75.2 us, 96 % of the copy rate; 1111 rows of 5120: 9.9 us (61 %: a row
+// to a block and five blocks to an SM, 740 of the 1111 at once, each a load, a reduction and a
+// store long, and a sixth of the threads' places for chunks empty); one row 2.3 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -106,7 +107,7 @@ __device__ __forceinline__ float norm_scale(float top, float ssq, int K, float e
 // (the second time h, from where this thread wrote it, or x).
 //
 // Blocks per SM: what the registers of the chunks allow.  (A row of three chunks and eight warps
-// would take 50, four blocks: 1111 rows of 5120 in 8.8 us; in 48, five blocks and a spilled
+// would take 50, four blocks: 1111 rows of 5120, in L2, 8.8 us; in 48, five blocks and a spilled
 // pointer, 8.7, and 8.5 by a maximum that drops NaN.)
 constexpr int resident(int cpt) { return cpt == 8 ? 2 : cpt == 6 ? 3 : cpt == 4 ? 4 : cpt == 3 ? 5 : 6; }
 

@@ -10,9 +10,10 @@
 //
 // Bound: HBM, 2 bytes read and 2 written per element.  A block turns the heads
 // of one or more tokens: it makes the tokens' rot / 2 angles once, in shared
-// memory, and every head reads them there.  14040 tokens of 48 heads of 128, 32 of
-// them rotated: 61 us, 87 % of the copy rate (one chunk at a time 81 us; four or six
-// blocks per SM instead of five 64 and 66).
+// memory, and every head reads them there.  14040 tokens of 48 heads of 128, 32
+// dims rotated in pairs: 61 us, 86 % of the copy rate (one chunk at a time 81 us; four or six
+// blocks per SM instead of five 64 and 66); all 128 in halves 59 us, in pairs 62; 32 in halves
+// 70 us (75 %: two steps are in flight there, and one that is copied loads one chunk).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
